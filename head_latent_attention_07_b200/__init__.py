@@ -16,6 +16,13 @@ importing the binding fails loudly when the shared library has not been built.
     mla.mla_decode_attn(dims, q_lat, pool, page_table, seq_lens, w_uv, workspace, out, lse)
     mla.mla_out_proj(dims, out, w_o, y)                       # layer output (optional)
 
+A cache kept within a budget (after a decode, whose lse is needed): mass of the
+cached tokens, choice of those that stay, compaction to them.
+
+    mla.mla_attn_mass(dims, q_lat, pool, page_table, seq_lens, lse, mass)
+    mla.mla_evict_select(mass, seq_lens, budgets, keep_idx, new_lens, n_sink=4, n_recent=512)
+    mla.mla_cache_compact(dims, pool, page_table, seq_lens, keep_idx, new_lens, mass=mass)
+
 Context split of long sequences over ranks: mla_decode_attn_partial on each
 rank's window, then mla_merge_ranks (see context_split.py for the process-group
 form).
@@ -39,6 +46,7 @@ MLA_ERR_RANGE = -7
 # Every entry point declared in include/mla.h, with its ctypes signature.
 _P = ctypes.c_void_p
 _I = ctypes.c_int32
+_L = ctypes.c_int64
 SIGNATURES = {
     "mla_append_latent": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, _I, _I, _P, _I, _I, _P, _P]),
     "mla_absorb_q": (ctypes.c_int, [_P, _P, _P, _P, _P, _I, _P]),
@@ -53,6 +61,9 @@ SIGNATURES = {
                                        _P, _P, _P, _P]),
     "mla_out_proj": (ctypes.c_int, [_P, _P, _P, _P, _I, _P]),
     "mla_query_proj": (ctypes.c_int, [_P, _I, _P, _P, _P, _P, _P, _I, _P]),
+    "mla_attn_mass": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, _I, _I, _I, _I, ctypes.c_float, _P, _P, _L, _P, _P]),
+    "mla_evict_select": (ctypes.c_int, [_P, _L, _P, _P, _I, _I, _I, _P, _L, _P, _P, _P]),
+    "mla_cache_compact": (ctypes.c_int, [_P, _P, _P, _P, _P, _L, _P, _I, _I, _I, _I, _P, _L, _P, _P]),
     "mla_status_read": (ctypes.c_int, [_P, _P]),
     "mla_status_clear": (ctypes.c_int, [_P, _P]),
     "mla_status_string": (ctypes.c_char_p, [ctypes.c_int]),
@@ -360,6 +371,99 @@ def mla_query_proj(dims: MlaDims, h, w_dq, w_uq, c_q, q, stream=None) -> None:
         _ptr(w_uq, torch.bfloat16, "w_uq"), _ptr(c_q, torch.bfloat16, "c_q"), _ptr(q, torch.bfloat16, "q"),
         T, _stream(stream))
     _check(st, "mla_query_proj")
+
+
+def _table(t, dtype, batch, name):
+    """Pointer and row length of a [batch, n] tensor."""
+    p = _ptr(t, dtype, name, ndim=2)
+    if t.shape[0] != batch:
+        raise ValueError(f"{name} must have {batch} rows, got shape {tuple(t.shape)}")
+    return p, t.shape[1]
+
+
+def _one_device(**tensors):
+    """All tensors on the current device (where the launch goes)."""
+    here = _torch().cuda.current_device()
+    for name, t in tensors.items():
+        if t is not None and t.is_cuda and t.device.index != here:
+            raise ValueError(f"{name} is on {t.device}, the current device is cuda:{here}")
+
+
+def mla_attn_mass(dims: MlaDims, q_lat, pool, page_table, seq_lens, lse, mass, mass_lens=None, decay: float = 1.0,
+                  dev_status=None, stream=None) -> None:
+    """Add the attention weights of q_lat [B, nq, H, d_c+d_rope] (summed over query tokens
+    and heads) to the cached tokens' mass [B, >= max_pages * page_size], the old mass times
+    `decay` first.  lse [B, nq, H] is mla_decode_attn's."""
+    torch = _torch()
+    B, nq = q_lat.shape[0], q_lat.shape[1]
+    _shape(q_lat, (B, nq, dims.n_heads, dims.row), "q_lat")
+    num_pages = pool.shape[0]
+    _shape(pool, (num_pages, dims.page_size, dims.row), "pool")
+    if page_table.dim() != 2 or page_table.shape[0] != B:
+        raise ValueError("page_table must be [B, max_pages]")
+    max_pages = page_table.shape[1]
+    _shape(seq_lens, (B,), "seq_lens")
+    _shape(lse, (B, nq, dims.n_heads), "lse")
+    if mass_lens is not None:
+        _shape(mass_lens, (B,), "mass_lens")
+    p_mass, mass_stride = _table(mass, torch.float32, B, "mass")
+    if mass_stride < max_pages * dims.page_size:
+        raise ValueError(f"mass rows must hold max_pages * page_size = {max_pages * dims.page_size} tokens")
+    _one_device(q_lat=q_lat, pool=pool, page_table=page_table, seq_lens=seq_lens, lse=lse, mass=mass,
+                mass_lens=mass_lens, dev_status=dev_status)
+    st = load_library().mla_attn_mass(
+        ctypes.byref(dims), _ptr(q_lat, torch.bfloat16, "q_lat"), _ptr(pool, torch.bfloat16, "pool"),
+        _ptr(page_table, torch.int32, "page_table"), _ptr(seq_lens, torch.int32, "seq_lens"),
+        _ptr(lse, torch.float32, "lse"), B, nq, max_pages, num_pages, decay,
+        _ptr(mass_lens, torch.int32, "mass_lens"), p_mass, mass_stride,
+        _ptr(dev_status, torch.int32, "dev_status"), _stream(stream))
+    _check(st, "mla_attn_mass")
+
+
+def mla_evict_select(mass, seq_lens, budgets, keep_idx, new_lens, n_sink: int = 0, n_recent: int = 0,
+                     dev_status=None, stream=None) -> None:
+    """keep_idx[b, :new_lens[b]] = the tokens of sequence b that stay within budgets[b]: the
+    first n_sink, the last n_recent and the largest of the rest by mass, ascending."""
+    torch = _torch()
+    B = seq_lens.shape[0]
+    _shape(seq_lens, (B,), "seq_lens")
+    _shape(budgets, (B,), "budgets")
+    _shape(new_lens, (B,), "new_lens")
+    if not (0 <= n_sink < 2**31 and 0 <= n_recent < 2**31):
+        raise ValueError(f"n_sink and n_recent must be in [0, 2^31), got {n_sink}, {n_recent}")
+    p_mass, mass_stride = _table(mass, torch.float32, B, "mass")
+    p_keep, keep_stride = _table(keep_idx, torch.int32, B, "keep_idx")
+    _one_device(mass=mass, seq_lens=seq_lens, budgets=budgets, keep_idx=keep_idx, new_lens=new_lens,
+                dev_status=dev_status)
+    st = load_library().mla_evict_select(
+        p_mass, mass_stride, _ptr(seq_lens, torch.int32, "seq_lens"), _ptr(budgets, torch.int32, "budgets"), B,
+        n_sink, n_recent, p_keep, keep_stride, _ptr(new_lens, torch.int32, "new_lens"),
+        _ptr(dev_status, torch.int32, "dev_status"), _stream(stream))
+    _check(st, "mla_evict_select")
+
+
+def mla_cache_compact(dims: MlaDims, pool, page_table, seq_lens, keep_idx, new_lens, mass=None,
+                      rerotate: bool = True, dev_status=None, stream=None) -> None:
+    """Move cache row keep_idx[b, j] of every sequence to row j (and its mass), in place;
+    with `rerotate` the RoPE part is turned to the new position."""
+    torch = _torch()
+    B, max_pages = page_table.shape
+    num_pages = pool.shape[0]
+    _shape(pool, (num_pages, dims.page_size, dims.row), "pool")
+    _shape(seq_lens, (B,), "seq_lens")
+    _shape(new_lens, (B,), "new_lens")
+    p_keep, keep_stride = _table(keep_idx, torch.int32, B, "keep_idx")
+    p_mass, mass_stride = (None, 0) if mass is None else _table(mass, torch.float32, B, "mass")
+    if mass is not None and mass_stride < max_pages * dims.page_size:
+        raise ValueError(f"mass rows must hold max_pages * page_size = {max_pages * dims.page_size} tokens")
+    _one_device(pool=pool, page_table=page_table, seq_lens=seq_lens, keep_idx=keep_idx, new_lens=new_lens, mass=mass,
+                dev_status=dev_status)
+    st = load_library().mla_cache_compact(
+        ctypes.byref(dims), _ptr(pool, torch.bfloat16, "pool"), _ptr(page_table, torch.int32, "page_table"),
+        _ptr(seq_lens, torch.int32, "seq_lens"), p_keep, keep_stride, _ptr(new_lens, torch.int32, "new_lens"),
+        B, max_pages, num_pages, 1 if rerotate else 0, p_mass, mass_stride,
+        _ptr(dev_status, torch.int32, "dev_status"), _stream(stream))
+    _check(st, "mla_cache_compact")
 
 
 def mla_status_read(dev_status, stream=None) -> int:

@@ -12,6 +12,9 @@
  * output W_O concat_h(o_h), after mla_decode_attn).  For sequences too long
  * for one GPU, mla_decode_attn_partial (one rank's window of the pages) and
  * mla_merge_ranks (the ranks' partials merged, then W_UV) split the key range.
+ * To keep the cache within a budget, between steps: mla_attn_mass (how much
+ * attention each cached token got), mla_evict_select (which tokens stay) and
+ * mla_cache_compact (the cache compacted to them, in place).
  * Keys and values are never decompressed: every cached token holds only its
  * latent c_t (d_c scalars) and its decoupled RoPE key k_t^R (d_rope scalars).
  *
@@ -334,6 +337,99 @@ int mla_out_proj(const mla_dims* dims, const mla_bf16* o, const mla_bf16* w_o, m
  */
 int mla_query_proj(const mla_dims* dims, int32_t q_lora_rank, const mla_bf16* h, const mla_bf16* w_dq,
                    const mla_bf16* w_uq, mla_bf16* c_q, mla_bf16* q, int32_t n_tokens, void* stream);
+
+/*
+ * mla_attn_mass - attention mass of the cached tokens.
+ *
+ * After mla_decode_attn returned the log-sum-exp of its rows, the attention weight
+ * of key n for query token i and head h is exp(s_n - lse[b][i][h]), s_n as there.
+ * This call sums it over the step's query tokens and heads and adds it to what the
+ * token collected before:
+ *   w    = sum_{i < nq} sum_{h < H} [n <= seq_lens[b] - nq + i] exp(s_n - lse[b][i][h])
+ *   mass[b][n] = decay * mass[b][n] + w      for n <  mass_lens[b]
+ *   mass[b][n] = w                           for n >= mass_lens[b]
+ * for 0 <= n < seq_lens[b]; later entries are left as they were.  A latent row is
+ * shared by all heads, so one number per token decides about it.
+ *
+ *   q_lat      device bf16 [batch, nq, H, d_c + d_rope], the step's absorbed queries (or
+ *              those of the last nq tokens of a chunk: an observation window)
+ *   pool, page_table, seq_lens   as for mla_decode_attn
+ *   lse        device fp32 [batch, nq, H], as returned by mla_decode_attn for these
+ *              queries; a row with lse = -inf (it saw no key) gives nothing
+ *   decay      0..1: 1 accumulates, less lets old mass fade, 0 starts anew (old
+ *              mass is then not read)
+ *   mass_lens  device int32 [batch]: leading tokens whose mass is meaningful, or NULL
+ *              for seq_lens[b] - nq (mass was taken at the step before)
+ *   mass       device fp32 [batch, mass_stride] (updated in place); row b starts
+ *              at mass + b * mass_stride, mass_stride >= max_pages * page_size
+ *   dev_status device int32 word or NULL
+ * Sums are fp32, in an order that does not depend on the schedule.  A sequence
+ * whose length is out of range (see mla_decode_attn) and the tokens of a page
+ * outside the pool keep their mass; both record MLA_ERR_RANGE.  batch and nq as
+ * for mla_decode_attn.
+ */
+int mla_attn_mass(const mla_dims* dims, const mla_bf16* q_lat, const mla_bf16* pool, const int32_t* page_table,
+                  const int32_t* seq_lens, const float* lse, int32_t batch, int32_t nq, int32_t max_pages,
+                  int32_t num_pages, float decay, const int32_t* mass_lens, float* mass, int64_t mass_stride,
+                  int32_t* dev_status, void* stream);
+
+/*
+ * mla_evict_select - the tokens that stay within a budget.
+ *
+ * For sequence b of L = seq_lens[b] tokens, new_lens[b] = K = min(L, budgets[b]).  Of its
+ * tokens stay: the first s = min(n_sink, K), the last r = min(n_recent, K - s),
+ * and of the others the K - s - r with the largest mass (equal masses: the lowest
+ * index first; -0 equals +0; NaN counts above +inf).  keep_idx[b][0..K) are their
+ * cache indices in ascending order; later entries are left as they were.
+ *
+ *   mass       device fp32 [batch, mass_stride] (see mla_attn_mass)
+ *   seq_lens   device int32 [batch], 0..mass_stride
+ *   budgets    device int32 [batch], >= 0
+ *   keep_idx   device int32 [batch, keep_stride] (output); row b starts at keep_idx +
+ *              b * keep_stride, keep_stride >= min(L, budgets[b])
+ *   new_lens   device int32 [batch] (output; must not overlap seq_lens or budgets)
+ *   dev_status device int32 word or NULL
+ * A sequence whose length, budget or K is out of range records MLA_ERR_RANGE and
+ * gets new_lens = 0.  batch <= 1024 and mass_stride <= 2^30 (else
+ * MLA_ERR_UNSUPPORTED).
+ */
+int mla_evict_select(const float* mass, int64_t mass_stride, const int32_t* seq_lens, const int32_t* budgets,
+                     int32_t batch, int32_t n_sink, int32_t n_recent, int32_t* keep_idx, int64_t keep_stride,
+                     int32_t* new_lens, int32_t* dev_status, void* stream);
+
+/*
+ * mla_cache_compact - the cache compacted to the tokens that stay, in place.
+ *
+ * For every sequence b and 0 <= j < new_lens[b], with n = keep_idx[b][j]:
+ *   cache row j = [c_n || RoPE(k_n^R, j - n)]    mass[b][j] = mass[b][n]
+ * (all right-hand sides before the call).  With rerotate = 1 the RoPE part is
+ * turned by the j - n positions that the token moved, so that the compacted cache
+ * is again one whose positions are its cache indices, and the next tokens are
+ * appended and queried at new_lens[b] and on; each move rounds the RoPE part to bf16
+ * once more.  With rerotate = 0 rows move bit for bit and keep the rotation they
+ * were appended with, for callers that keep positions of their own.  Rows from
+ * new_lens[b] on are left as they were; the sequence's pages from
+ * ceil(new_lens[b] / page_size) on are free.
+ *
+ *   pool       device bf16 [num_pages, page_size, d_c + d_rope] (updated in place); a page
+ *              of a sequence that moves rows must belong to no other sequence
+ *   page_table device int32 [batch, max_pages]
+ *   seq_lens   device int32 [batch]: lengths before the call, 0..max_pages * page_size
+ *   keep_idx   device int32 [batch, keep_stride], j <= keep_idx[b][j] < seq_lens[b]: as
+ *              written by mla_evict_select, or any other choice in ascending order
+ *   new_lens   device int32 [batch], 0..min(seq_lens[b], keep_stride)
+ *   mass       device fp32 [batch, mass_stride] (updated in place) or NULL;
+ *              mass_stride >= max_pages * page_size
+ *   dev_status device int32 word or NULL
+ * Rows with keep_idx[b][j] == j are not touched.  An index outside [j, seq_lens[b])
+ * or a page outside the pool records MLA_ERR_RANGE and row j stays as it was; a
+ * sequence whose lengths are out of range records it and is left alone.
+ * batch <= 1024 (else MLA_ERR_UNSUPPORTED).
+ */
+int mla_cache_compact(const mla_dims* dims, mla_bf16* pool, const int32_t* page_table, const int32_t* seq_lens,
+                      const int32_t* keep_idx, int64_t keep_stride, const int32_t* new_lens, int32_t batch,
+                      int32_t max_pages, int32_t num_pages, int32_t rerotate, float* mass, int64_t mass_stride,
+                      int32_t* dev_status, void* stream);
 
 /* mla_status_read - wait for `stream`, then return the mla_status recorded in the
  * device word dev_status (MLA_OK if none), or MLA_ERR_CUDA if the copy failed. */

@@ -12,6 +12,8 @@ Contents:
                        authority), the absorbed form, a brute-force loop form,
                        split-KV partials with a log-sum-exp merge, and paged
                        cache gathering.
+  eviction.py          attention mass of the cached tokens, the choice of those
+                       that stay within a budget, compaction of the cache.
   cache_accounting.py  closed-form KV-cache sizes per architecture.
 
 Every function says which page and section it follows.  Pages cited:
@@ -25,4 +27,4 @@ Every function says which page and section it follows.  Pages cited:
 Parity status: every function here is pinned by a `-m "not gpu"` test against
 closed forms, hand-derived fixtures, invariants or brute force (tests/test_oracle_*.py).
 """
-from . import mla, cache_accounting  # noqa: F401
+from . import mla, eviction, cache_accounting  # noqa: F401
