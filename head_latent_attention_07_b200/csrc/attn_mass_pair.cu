@@ -1,0 +1,447 @@
+// Attention mass of the cached tokens on CTA pairs with 2-SM tensor-core
+// instructions (tcgen05 .cta_group::2, TMEM, TMA).
+//
+// Shape: d_c = 512, d_rope = 64 (576-wide cache rows), 64-token pages.  The product is
+// transposed against the decode kernel's: the keys are its rows and the query
+// rows its columns, S[256 x NT] = K[256 x 576] . Q[NT x 576]^T, so a key's scores lie in
+// one TMEM lane and one thread adds up its weights: no reduction across threads,
+// no running maximum (the lse is final) and a fixed order of the sum.
+//
+//   tile    256 keys of a sequence (4 pages), 128 per CTA of the pair
+//   group   NT query rows (128 or 256), half of them in each CTA's shared memory
+// The keys stream: blocks of [128 keys x 64 columns] (16 KB) go by TMA through a ring,
+// and each is done with after its four MMAs.  A group's query stays in shared memory
+// (9 blocks) for as many tiles as possible; where a sequence has more than one group
+// (nq * H > 256), the worker takes kSubTiles tiles at a time through all groups, so that the
+// groups after the first find the keys in L2.  A query block is reloaded as soon as the
+// last tile of its group is through with that block.
+//
+// With one group the bound is HBM: 1152 bytes per key against 256 x NT x 576 products per
+// tile, about 4600 cycles of the tensor pipe at NT = 256 for 295 KB per pair, which takes
+// 6700 at the pair's share of the bandwidth.  With many groups the tensor pipe is.
+//
+// TMEM: two accumulators of NT columns, so that the sum over one tile runs beside the
+// next tile's MMAs.  Warps (256 threads): 0 loads (TMA), 1 owns TMEM and, in CTA 0, issues
+// the MMAs, 2 brings the groups' lse, 4-7 sum (warp w reads TMEM lanes 32 (w & 3) and on).  Every mbarrier wait is
+// bounded: on time-out the kernel records MLA_ERR_TIMEOUT, drains its MMAs and ends.
+#include <cuda.h>
+
+#include "common.cuh"
+#include "evict.h"
+#include "plan.cuh"
+#include "sm100.cuh"
+
+namespace mla {
+
+namespace {
+
+using namespace sm100;
+
+constexpr int kThreads = 256;
+constexpr int kTileKeys = 256;
+constexpr int kBlocks = 9;                       // 64-column blocks of a 576-wide row
+constexpr int kKeyBytes = 128 * 128;             // [128 keys x 64 columns] bf16, 128-byte swizzle
+constexpr int kSubTiles = 4;                     // tiles per pass over the groups: 74 pairs hold 87 MB of keys in L2
+constexpr long long kDrainCycles = 1ll << 24;
+
+template <int NT>
+struct Layout {
+  static constexpr int kQBytes = NT / 2 * 128;                       // one block of this CTA's half of the group
+  static constexpr int kStages = NT == 256 ? 5 : 9;
+  static constexpr int kOffK = kBlocks * kQBytes;
+  static constexpr int kOffLse = kOffK + kStages * kKeyBytes;        // fp32 [NT], log2 units
+  static constexpr int kOffBar = kOffLse + NT * 4;
+  static constexpr int kBytes = kOffBar + 512 + 1024;                // + 1 KB alignment slack
+};
+static_assert(Layout<256>::kBytes <= 232448 && Layout<128>::kBytes <= 232448, "shared memory budget");
+
+struct Bars {
+  uint64_t k_full[9];    // CTA 0: both CTAs' key blocks landed in the stage (2 arrivals + bytes)
+  uint64_t k_empty[9];   // both: the MMAs are done with the stage
+  uint64_t q_full[9];    // CTA 0: both CTAs' halves of a query block landed
+  uint64_t q_empty[9];   // both: the group's MMAs are done with the query block
+  uint64_t acc_full[2];  // both: a tile's scores are in TMEM
+  uint64_t acc_empty[2]; // CTA 0: the 8 summing warps of the pair have read them
+  uint64_t lse_full;     // local: a group's lse is in shared memory
+  uint64_t lse_empty;    // local: the 4 summing warps have read the last group's
+  uint64_t drain;        // both: every MMA issued has completed
+  uint32_t tmem_base;
+  int abort;
+  int b0, tile0;         // where this worker starts
+};
+static_assert(sizeof(Bars) <= 512, "barrier area");
+
+struct PairMassParams {
+  MassArgs m;
+  int rows_total;        // nq * H
+  int groups;
+  float scale_log2;
+  long long spin_limit;
+};
+
+// A sequence's tiles; 0 when its length is out of range.
+__device__ __forceinline__ int seq_tiles(const MassArgs& a, int b, int* len) {
+  *len = a.seq_lens[b];
+  return *len < a.nq || *len > a.max_pages * 64 ? 0 : (*len + kTileKeys - 1) / kTileKeys;
+}
+
+// One accumulator's worth of work; every role walks the same ones in the same order.
+struct Item {
+  int b, len, tile, group;
+  bool first, last;      // of the tiles that see this group's query in shared memory
+};
+struct Cursor {
+  const PairMassParams& p;
+  int b, tile, left;     // next sequence and tile, tiles left of this worker's share
+  int len = 0, sub0 = 0, sub1 = 0, t = 0, g = 0;
+  __device__ Cursor(const PairMassParams& p_, const Bars* bar, int share) : p(p_), b(bar->b0), tile(bar->tile0), left(share) {}
+  __device__ bool next(Item* it) {
+    if (t == sub1) {                             // the group's tiles are done
+      ++g;
+      if (g >= p.groups || sub1 == 0) {
+        if (left == 0) return false;
+        int n;
+        while (tile >= (n = seq_tiles(p.m, b, &len))) { ++b; tile = 0; }
+        sub0 = tile;
+        sub1 = min(n, tile + left);
+        if (p.groups > 1) sub1 = min(sub1, tile + kSubTiles);
+        left -= sub1 - sub0;
+        tile = sub1;
+        g = 0;
+      }
+      t = sub0;
+    }
+    it->b = b;
+    it->len = len;
+    it->tile = t;
+    it->group = g;
+    it->first = t == sub0;
+    ++t;
+    it->last = t == sub1;
+    return true;
+  }
+};
+
+__device__ __forceinline__ bool elect_one() {
+  uint32_t is_leader;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(is_leader));
+  return is_leader != 0;
+}
+
+template <int NT>
+__global__ void __launch_bounds__(kThreads, 1)
+attn_mass_pair_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tp,
+                      const __grid_constant__ PairMassParams prm) {
+  using L = Layout<NT>;
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* sm =
+      reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  float* lse2 = reinterpret_cast<float*>(sm + L::kOffLse);
+  Bars* bar = reinterpret_cast<Bars*>(sm + L::kOffBar);
+  volatile int* abort_flag = &bar->abort;
+
+  const MassArgs& a = prm.m;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t c = cluster_ctarank();
+  const int w = blockIdx.x >> 1, workers = gridDim.x >> 1;
+  const long long lim = prm.spin_limit;
+  int32_t* status = a.dev_status;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < 9; ++s) {
+      mbar_init(&bar->k_full[s], 2);
+      mbar_init(&bar->k_empty[s], 1);
+      mbar_init(&bar->q_full[s], 2);
+      mbar_init(&bar->q_empty[s], 1);
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&bar->acc_full[s], 1);
+      mbar_init(&bar->acc_empty[s], 8);
+    }
+    mbar_init(&bar->lse_full, 1);
+    mbar_init(&bar->lse_empty, 4);
+    mbar_init(&bar->drain, 1);
+    bar->abort = 0;
+    fence_mbar_init();
+    tma_prefetch(&tq);
+    tma_prefetch(&tp);
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(&bar->tmem_base, 2 * NT);
+    tmem_relinquish_pair();
+  }
+  grid_dependency_wait();
+  allow_dependent_launch();
+
+  // the tiles of all sequences end to end, an equal share for each worker: where
+  // does this one's start?  (lse2 serves as scratch)
+  int total = 0, share = 0;
+  {
+    int* scratch = reinterpret_cast<int*>(lse2);
+    for (int base = 0; base < a.batch; base += kThreads) {
+      const int b = base + threadIdx.x;
+      int len, tot;
+      const int v = b < a.batch ? seq_tiles(a, b, &len) : 0;
+      if (b < a.batch && v == 0 && blockIdx.x == 0) record_status(status, MLA_ERR_RANGE);
+      block_exclusive_scan(v, scratch, &tot);
+      total += tot;
+    }
+    const int t0 = (int)((long long)total * w / workers);
+    share = (int)((long long)total * (w + 1) / workers) - t0;
+    int carry = 0;
+    for (int base = 0; base < a.batch && carry <= t0; base += kThreads) {
+      const int b = base + threadIdx.x;
+      int len, tot;
+      const int v = b < a.batch ? seq_tiles(a, b, &len) : 0;
+      const int at = carry + block_exclusive_scan(v, scratch, &tot);
+      if (v > 0 && at <= t0 && t0 < at + v) {
+        bar->b0 = b;
+        bar->tile0 = t0 - at;
+      }
+      carry += tot;
+    }
+  }
+  __syncthreads();
+  tc_fence_before();
+  cluster_sync();        // barriers and TMEM of both CTAs ready before any remote traffic
+  tc_fence_after();
+  const uint32_t tmem = bar->tmem_base;
+  auto wwait = [&](uint64_t* b, uint32_t parity) -> bool {
+    return __all_sync(0xffffffffu, mbar_wait(b, parity, abort_flag, status, lim));
+  };
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ queries and keys (TMA)
+    const uint32_t kfull0 = mapa(smem_u32(&bar->k_full[0]), 0);
+    const uint32_t qfull0 = mapa(smem_u32(&bar->q_full[0]), 0);
+    const int oob_row = a.num_pages * 64;        // a box starting here lies outside the pool: zero fill
+    const uint64_t once = l2_policy_evict_first();
+    Cursor cur(prm, bar, share);
+    Item it;
+    int k = 0, gi = -1;                          // stages used, groups begun
+    bool ok = true;
+    while (ok && cur.next(&it)) {
+      if (it.first) ++gi;
+      int y[2];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int pg = it.tile * 4 + (int)c * 2 + j;
+        y[j] = oob_row;
+        if (pg * 64 < it.len) {
+          const int id = a.page_table[(size_t)it.b * a.max_pages + pg];
+          if (id >= 0 && id < a.num_pages) y[j] = id * 64;
+          else if (lane == 0) record_status(status, MLA_ERR_RANGE);
+        }
+      }
+      const int qrow = it.b * prm.rows_total + it.group * NT + (int)c * (NT / 2);
+      for (int blk = 0; blk < kBlocks; ++blk, ++k) {
+        if (it.first) {
+          if (gi > 0 && !(ok = wwait(&bar->q_empty[blk], (gi - 1) & 1))) break;
+          if (lane == 0) {
+            mbar_arrive_expect_tx_cluster(qfull0 + 8 * blk, L::kQBytes);
+            tma_load_2d_pair(sm + blk * L::kQBytes, &tq, 64 * blk, qrow, qfull0 + 8 * blk);
+          }
+        }
+        const int s = k % L::kStages;
+        if (k >= L::kStages && !(ok = wwait(&bar->k_empty[s], (k / L::kStages - 1) & 1))) break;
+        if (lane == 0) {
+          unsigned char* dst = sm + L::kOffK + s * kKeyBytes;
+          mbar_arrive_expect_tx_cluster(kfull0 + 8 * s, kKeyBytes);
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            if (prm.groups == 1)
+              tma_load_2d_pair_hint(dst + j * (kKeyBytes / 2), &tp, 64 * blk, y[j], kfull0 + 8 * s, once);
+            else
+              tma_load_2d_pair(dst + j * (kKeyBytes / 2), &tp, 64 * blk, y[j], kfull0 + 8 * s);
+          }
+        }
+        __syncwarp();
+      }
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issuer (CTA 0)
+    if (c == 0) {
+      const uint32_t idesc = idesc_bf16_f32(256, NT, 0, 0);
+      const uint32_t qa = smem_u32(sm), ka = smem_u32(sm + L::kOffK);
+      Cursor cur(prm, bar, share);
+      Item it;
+      int k = 0, gi = -1, t = 0;
+      bool ok = true;
+      while (ok && cur.next(&it)) {
+        if (it.first) ++gi;
+        if (t >= 2 && !wwait(&bar->acc_empty[t & 1], ((t >> 1) - 1) & 1)) break;
+        const uint32_t d = tmem + (t & 1) * NT;
+        for (int blk = 0; blk < kBlocks; ++blk, ++k) {
+          const int s = k % L::kStages;
+          if (it.first && !(ok = wwait(&bar->q_full[blk], gi & 1))) break;
+          if (!(ok = wwait(&bar->k_full[s], (k / L::kStages) & 1))) break;
+          tc_fence_after();
+          if (elect_one()) {
+#pragma unroll
+            for (int ks = 0; ks < 4; ++ks) {
+              const uint64_t da = smem_desc(ka + s * kKeyBytes + ks * 32, 16, 1024, kSwizzle128);
+              const uint64_t db = smem_desc(qa + blk * L::kQBytes + ks * 32, 16, 1024, kSwizzle128);
+              mma_bf16_pair(d, da, db, idesc, blk + ks > 0 ? 1u : 0u);
+            }
+            mma_commit_pair(&bar->k_empty[s]);
+            if (it.last) mma_commit_pair(&bar->q_empty[blk]);
+            if (blk == kBlocks - 1) mma_commit_pair(&bar->acc_full[t & 1]);
+          }
+          __syncwarp();
+        }
+        ++t;
+      }
+      // every MMA and every earlier commit has completed before TMEM and shared memory go away
+      if (elect_one()) mma_commit_pair(&bar->drain);
+      __syncwarp();
+    }
+    if (lane == 0) mbar_wait_drain(&bar->drain, 0, kDrainCycles + lim);
+    __syncwarp();
+  } else if (warp == 2) {
+    // ------------------------------------------------------------ lse of a group's query rows
+    Cursor cur(prm, bar, share);
+    Item it;
+    int gi = 0;
+    while (cur.next(&it)) {
+      if (!it.first) continue;
+      const int cols = prm.rows_total - it.group * NT;
+      const float* src = a.lse + (size_t)it.b * prm.rows_total + it.group * NT;
+      float l[NT / 32];
+#pragma unroll
+      for (int i = 0; i < NT / 32; ++i) {
+        // a row that saw no key (lse = -inf) gives nothing: exp2(x - inf) = 0
+        l[i] = i * 32 + lane < cols ? src[i * 32 + lane] : INFINITY;
+        l[i] = l[i] == -INFINITY ? INFINITY : l[i] * 1.4426950408889634f;
+      }
+      if (gi > 0 && !wwait(&bar->lse_empty, (gi - 1) & 1)) break;
+#pragma unroll
+      for (int i = 0; i < NT / 32; ++i) lse2[i * 32 + lane] = l[i];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar->lse_full);
+      ++gi;
+    }
+  } else if (warp >= 4) {
+    // ------------------------------------------------------------ weights and their sum
+    const uint32_t acc_empty0 = mapa(smem_u32(&bar->acc_empty[0]), 0);
+    const uint32_t lanes = tmem + (uint32_t((warp & 3) * 32) << 16);
+    Cursor cur(prm, bar, share);
+    Item it;
+    int t = 0, gi = -1;
+    while (cur.next(&it)) {
+      const int cols = min(NT, prm.rows_total - it.group * NT);
+      if (it.first) {
+        ++gi;
+        if (!wwait(&bar->lse_full, gi & 1)) break;
+      }
+      // this thread's key, its page and what it has collected so far
+      const int n = it.tile * kTileKeys + (int)c * 128 + (warp & 3) * 32 + lane;
+      float* m = a.mass + (size_t)it.b * a.mass_stride + n;
+      bool live = n < it.len;
+      float old = 0.f;
+      if (live) {
+        const int id = a.page_table[(size_t)it.b * a.max_pages + (n >> 6)];
+        live = id >= 0 && id < a.num_pages;
+        if (it.group > 0) old = *m;              // the earlier groups' sum (decay is in it)
+        else if (a.decay != 0.f && n < (a.mass_lens != nullptr ? a.mass_lens[it.b] : it.len - a.nq)) old = a.decay * *m;
+      }
+      if (!wwait(&bar->acc_full[t & 1], (t >> 1) & 1)) break;
+      tc_fence_after();
+      const uint32_t acc = lanes + (t & 1) * NT;
+      // key n is seen by query i when n <= len - nq + i: by query rows from H * (n - (len - nq)) on
+      const int first = max(0, n - (it.len - a.nq)) * a.n_heads - it.group * NT;
+      const bool all = __all_sync(0xffffffffu, first <= 0);
+      float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+      for (int c0 = 0; c0 < cols; c0 += 32) {
+        float v[32];
+        tmem_ld32(acc + c0, v);
+        tmem_wait_ld();
+        if (all && c0 + 32 <= cols) {
+#pragma unroll
+          for (int i = 0; i < 32; i += 4) {
+            const float4 l = *reinterpret_cast<const float4*>(lse2 + c0 + i);
+            sum[0] += ex2(fmaf(v[i], prm.scale_log2, -l.x));
+            sum[1] += ex2(fmaf(v[i + 1], prm.scale_log2, -l.y));
+            sum[2] += ex2(fmaf(v[i + 2], prm.scale_log2, -l.z));
+            sum[3] += ex2(fmaf(v[i + 3], prm.scale_log2, -l.w));
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            const float e = ex2(fmaf(v[i], prm.scale_log2, -lse2[c0 + i]));
+            if (c0 + i >= first && c0 + i < cols) sum[i & 3] += e;
+          }
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive_cluster(acc_empty0 + 8 * (t & 1));
+        if (it.last) mbar_arrive(&bar->lse_empty);
+      }
+      if (live) *m = old + ((sum[0] + sum[1]) + (sum[2] + sum[3]));
+      ++t;
+    }
+  }
+
+  // ------------------------------------------------------------ teardown
+  tc_fence_before();
+  __syncthreads();
+  if (*abort_flag) {
+    // after a time-out, copies this CTA issued may still be in flight (their
+    // completion is counted in CTA 0): give them time to land before exiting
+    const long long t0 = clock64();
+    while (clock64() - t0 < 200000) __nanosleep(1000);
+  }
+  cluster_sync();        // the peer no longer touches this CTA's shared memory or TMEM
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem, 2 * NT);
+  }
+}
+
+template <int NT>
+cudaError_t launch(const CUtensorMap& tq, const CUtensorMap& tp, const PairMassParams& prm, int workers,
+                   cudaStream_t stream) {
+  cudaError_t e = cudaFuncSetAttribute(attn_mass_pair_kernel<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       Layout<NT>::kBytes);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2 * workers, 1, 1);
+  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.dynamicSmemBytes = Layout<NT>::kBytes;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1] = pdl_attribute();
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  e = cudaLaunchKernelEx(&cfg, attn_mass_pair_kernel<NT>, tq, tp, prm);
+  if (e != cudaSuccess) return e;
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_attn_mass_pair(const MassArgs& a, int sms, long long spin_limit, cudaStream_t stream) {
+  PairMassParams prm;
+  prm.m = a;
+  prm.rows_total = a.nq * a.n_heads;
+  const int nt = prm.rows_total > 128 ? 256 : 128;
+  prm.groups = (prm.rows_total + nt - 1) / nt;
+  prm.scale_log2 = a.scale * 1.4426950408889634f;
+  prm.spin_limit = spin_limit;
+  CUtensorMap tq, tp;
+  if (!encode_rows576(&tq, a.q_lat, (uint64_t)a.batch * prm.rows_total, 64, nt / 2, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !encode_rows576(&tp, a.pool, (uint64_t)a.num_pages * 64, 64, 64, CU_TENSOR_MAP_SWIZZLE_128B))
+    return cudaErrorInvalidValue;
+  // one pair per two SMs, but no more pairs than the batch can have tiles
+  const int64_t tiles = (int64_t)a.batch * ((a.max_pages + 3) / 4);
+  const int workers = (int)(tiles < sms / 2 ? tiles : sms / 2);
+  return nt == 256 ? launch<256>(tq, tp, prm, workers, stream) : launch<128>(tq, tp, prm, workers, stream);
+}
+
+}  // namespace mla

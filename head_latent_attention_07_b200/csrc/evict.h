@@ -48,6 +48,8 @@ struct CompactArgs {
   uint64_t turn[kMaxRopePairs];  // theta^(-2i/d_rope) / (2 pi) of pair i, as a fraction of a turn times 2^64
 };
 
+// Tensor-core pairs (the shapes of decode_pair_supported), and any other shape.
+cudaError_t launch_attn_mass_pair(const MassArgs& a, int sms, long long spin_limit, cudaStream_t stream);
 cudaError_t launch_attn_mass(const MassArgs& a, cudaStream_t stream);
 cudaError_t launch_evict_select(const SelectArgs& a, int sms, cudaStream_t stream);
 cudaError_t launch_cache_compact(const CompactArgs& a, int sms, cudaStream_t stream);

@@ -1,6 +1,7 @@
 // C ABI of the cache-eviction calls: argument validation and launches.  The
 // declarations and the contract of every entry point are in include/mla.h.
 #include <math.h>
+#include <stdlib.h>
 
 #include "../../include/mla.h"
 #include "evict.h"
@@ -43,6 +44,18 @@ int device_sms(int* sms) {
   return cuda_status(cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev));
 }
 
+// Spin budget of each bounded wait, as for the decode calls: kSpinLimitCycles, or the
+// environment variable MLA_SPIN_LIMIT (cycles, >= 0) when it is set.
+long long spin_limit_cycles() {
+  const char* e = getenv("MLA_SPIN_LIMIT");
+  if (e != nullptr && *e != 0) {
+    char* end = nullptr;
+    const long long v = strtoll(e, &end, 10);
+    if (end != nullptr && *end == 0 && v >= 0) return v;
+  }
+  return mla::kSpinLimitCycles;
+}
+
 }  // namespace
 
 extern "C" {
@@ -68,7 +81,11 @@ int mla_attn_mass(const mla_dims* dims, const mla_bf16* q_lat, const mla_bf16* p
   a.page_size = dims->page_size; a.max_pages = max_pages; a.num_pages = num_pages;
   a.scale = dims->softmax_scale > 0.f ? dims->softmax_scale : 1.0f / sqrtf((float)(dims->qk_nope + dims->d_rope));
   a.decay = decay;
-  return cuda_status(mla::launch_attn_mass(a, (cudaStream_t)stream));
+  if (!mla::decode_pair_supported(a.d_c, a.d_rope, a.page_size))
+    return cuda_status(mla::launch_attn_mass(a, (cudaStream_t)stream));
+  int sms = 0;
+  if ((st = device_sms(&sms)) != MLA_OK) return st;
+  return cuda_status(mla::launch_attn_mass_pair(a, sms, spin_limit_cycles(), (cudaStream_t)stream));
 }
 
 int mla_evict_select(const float* mass, int64_t mass_stride, const int32_t* seq_lens, const int32_t* budgets,
