@@ -373,20 +373,44 @@ def mla_query_proj(dims: MlaDims, h, w_dq, w_uq, c_q, q, stream=None) -> None:
     _check(st, "mla_query_proj")
 
 
-def _table(t, dtype, batch, name):
-    """Pointer and row length of a [batch, n] tensor."""
-    p = _ptr(t, dtype, name, ndim=2)
-    if t.shape[0] != batch:
-        raise ValueError(f"{name} must have {batch} rows, got shape {tuple(t.shape)}")
-    return p, t.shape[1]
+def _pointers(*specs):
+    """Data pointers of (tensor, dtype, shape, name) after the checks of all: type and shape
+    first, then that every tensor is dense and on the current device, where the call
+    launches.  An optional tensor that is None gives None."""
+    torch = _torch()
+    for t, dtype, shape, name in specs:
+        if t is None:
+            continue
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
+        if t.dtype != dtype:
+            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+        if shape is not None and t.shape != shape:
+            raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    device = None
+    out = []
+    for t, dtype, shape, name in specs:
+        if t is None:
+            out.append(None)
+            continue
+        index = t.get_device()
+        if index < 0:
+            raise ValueError(f"{name} must be a CUDA tensor")
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+        if device is None:
+            device = torch.cuda.current_device()
+        if index != device:
+            raise ValueError(f"{name} is on cuda:{index}, the current device is cuda:{device}")
+        out.append(t.data_ptr())
+    return out
 
 
-def _one_device(**tensors):
-    """All tensors on the current device (where the launch goes)."""
-    here = _torch().cuda.current_device()
-    for name, t in tensors.items():
-        if t is not None and t.is_cuda and t.device.index != here:
-            raise ValueError(f"{name} is on {t.device}, the current device is cuda:{here}")
+def _matrix(t, rows, name):
+    """Row length of a [rows, n] tensor."""
+    if t.dim() != 2 or t.shape[0] != rows:
+        raise ValueError(f"{name} must have shape ({rows}, n), got {tuple(t.shape)}")
+    return t.shape[1]
 
 
 def mla_attn_mass(dims: MlaDims, q_lat, pool, page_table, seq_lens, lse, mass, mass_lens=None, decay: float = 1.0,
@@ -395,28 +419,20 @@ def mla_attn_mass(dims: MlaDims, q_lat, pool, page_table, seq_lens, lse, mass, m
     and heads) to the cached tokens' mass [B, >= max_pages * page_size], the old mass times
     `decay` first.  lse [B, nq, H] is mla_decode_attn's."""
     torch = _torch()
+    i32, f32, bf16 = torch.int32, torch.float32, torch.bfloat16
     B, nq = q_lat.shape[0], q_lat.shape[1]
-    _shape(q_lat, (B, nq, dims.n_heads, dims.row), "q_lat")
+    H, row, page = dims.n_heads, dims.row, dims.page_size
+    max_pages = _matrix(page_table, B, "page_table")
+    width = _matrix(mass, B, "mass")
+    if width < max_pages * page:
+        raise ValueError(f"mass rows must hold max_pages * page_size = {max_pages * page} tokens, got {width}")
     num_pages = pool.shape[0]
-    _shape(pool, (num_pages, dims.page_size, dims.row), "pool")
-    if page_table.dim() != 2 or page_table.shape[0] != B:
-        raise ValueError("page_table must be [B, max_pages]")
-    max_pages = page_table.shape[1]
-    _shape(seq_lens, (B,), "seq_lens")
-    _shape(lse, (B, nq, dims.n_heads), "lse")
-    if mass_lens is not None:
-        _shape(mass_lens, (B,), "mass_lens")
-    p_mass, mass_stride = _table(mass, torch.float32, B, "mass")
-    if mass_stride < max_pages * dims.page_size:
-        raise ValueError(f"mass rows must hold max_pages * page_size = {max_pages * dims.page_size} tokens")
-    _one_device(q_lat=q_lat, pool=pool, page_table=page_table, seq_lens=seq_lens, lse=lse, mass=mass,
-                mass_lens=mass_lens, dev_status=dev_status)
-    st = load_library().mla_attn_mass(
-        ctypes.byref(dims), _ptr(q_lat, torch.bfloat16, "q_lat"), _ptr(pool, torch.bfloat16, "pool"),
-        _ptr(page_table, torch.int32, "page_table"), _ptr(seq_lens, torch.int32, "seq_lens"),
-        _ptr(lse, torch.float32, "lse"), B, nq, max_pages, num_pages, decay,
-        _ptr(mass_lens, torch.int32, "mass_lens"), p_mass, mass_stride,
-        _ptr(dev_status, torch.int32, "dev_status"), _stream(stream))
+    p = _pointers((q_lat, bf16, (B, nq, H, row), "q_lat"), (pool, bf16, (num_pages, page, row), "pool"),
+                  (page_table, i32, None, "page_table"), (seq_lens, i32, (B,), "seq_lens"),
+                  (lse, f32, (B, nq, H), "lse"), (mass_lens, i32, (B,), "mass_lens"), (mass, f32, None, "mass"),
+                  (dev_status, i32, None, "dev_status"))
+    st = load_library().mla_attn_mass(ctypes.byref(dims), p[0], p[1], p[2], p[3], p[4], B, nq, max_pages, num_pages,
+                                      decay, p[5], p[6], width, p[7], _stream(stream))
     _check(st, "mla_attn_mass")
 
 
@@ -425,20 +441,16 @@ def mla_evict_select(mass, seq_lens, budgets, keep_idx, new_lens, n_sink: int = 
     """keep_idx[b, :new_lens[b]] = the tokens of sequence b that stay within budgets[b]: the
     first n_sink, the last n_recent and the largest of the rest by mass, ascending."""
     torch = _torch()
+    i32 = torch.int32
     B = seq_lens.shape[0]
-    _shape(seq_lens, (B,), "seq_lens")
-    _shape(budgets, (B,), "budgets")
-    _shape(new_lens, (B,), "new_lens")
     if not (0 <= n_sink < 2**31 and 0 <= n_recent < 2**31):
         raise ValueError(f"n_sink and n_recent must be in [0, 2^31), got {n_sink}, {n_recent}")
-    p_mass, mass_stride = _table(mass, torch.float32, B, "mass")
-    p_keep, keep_stride = _table(keep_idx, torch.int32, B, "keep_idx")
-    _one_device(mass=mass, seq_lens=seq_lens, budgets=budgets, keep_idx=keep_idx, new_lens=new_lens,
-                dev_status=dev_status)
-    st = load_library().mla_evict_select(
-        p_mass, mass_stride, _ptr(seq_lens, torch.int32, "seq_lens"), _ptr(budgets, torch.int32, "budgets"), B,
-        n_sink, n_recent, p_keep, keep_stride, _ptr(new_lens, torch.int32, "new_lens"),
-        _ptr(dev_status, torch.int32, "dev_status"), _stream(stream))
+    width, keep = _matrix(mass, B, "mass"), _matrix(keep_idx, B, "keep_idx")
+    p = _pointers((mass, torch.float32, None, "mass"), (seq_lens, i32, (B,), "seq_lens"),
+                  (budgets, i32, (B,), "budgets"), (keep_idx, i32, None, "keep_idx"),
+                  (new_lens, i32, (B,), "new_lens"), (dev_status, i32, None, "dev_status"))
+    st = load_library().mla_evict_select(p[0], width, p[1], p[2], B, n_sink, n_recent, p[3], keep, p[4], p[5],
+                                         _stream(stream))
     _check(st, "mla_evict_select")
 
 
@@ -447,22 +459,19 @@ def mla_cache_compact(dims: MlaDims, pool, page_table, seq_lens, keep_idx, new_l
     """Move cache row keep_idx[b, j] of every sequence to row j (and its mass), in place;
     with `rerotate` the RoPE part is turned to the new position."""
     torch = _torch()
+    i32 = torch.int32
     B, max_pages = page_table.shape
-    num_pages = pool.shape[0]
-    _shape(pool, (num_pages, dims.page_size, dims.row), "pool")
-    _shape(seq_lens, (B,), "seq_lens")
-    _shape(new_lens, (B,), "new_lens")
-    p_keep, keep_stride = _table(keep_idx, torch.int32, B, "keep_idx")
-    p_mass, mass_stride = (None, 0) if mass is None else _table(mass, torch.float32, B, "mass")
-    if mass is not None and mass_stride < max_pages * dims.page_size:
-        raise ValueError(f"mass rows must hold max_pages * page_size = {max_pages * dims.page_size} tokens")
-    _one_device(pool=pool, page_table=page_table, seq_lens=seq_lens, keep_idx=keep_idx, new_lens=new_lens, mass=mass,
-                dev_status=dev_status)
-    st = load_library().mla_cache_compact(
-        ctypes.byref(dims), _ptr(pool, torch.bfloat16, "pool"), _ptr(page_table, torch.int32, "page_table"),
-        _ptr(seq_lens, torch.int32, "seq_lens"), p_keep, keep_stride, _ptr(new_lens, torch.int32, "new_lens"),
-        B, max_pages, num_pages, 1 if rerotate else 0, p_mass, mass_stride,
-        _ptr(dev_status, torch.int32, "dev_status"), _stream(stream))
+    num_pages, page = pool.shape[0], dims.page_size
+    keep = _matrix(keep_idx, B, "keep_idx")
+    width = 0 if mass is None else _matrix(mass, B, "mass")
+    if mass is not None and width < max_pages * page:
+        raise ValueError(f"mass rows must hold max_pages * page_size = {max_pages * page} tokens, got {width}")
+    p = _pointers((pool, torch.bfloat16, (num_pages, page, dims.row), "pool"), (page_table, i32, None, "page_table"),
+                  (seq_lens, i32, (B,), "seq_lens"), (keep_idx, i32, None, "keep_idx"),
+                  (new_lens, i32, (B,), "new_lens"), (mass, torch.float32, None, "mass"),
+                  (dev_status, i32, None, "dev_status"))
+    st = load_library().mla_cache_compact(ctypes.byref(dims), p[0], p[1], p[2], p[3], keep, p[4], B, max_pages, num_pages,
+                                          1 if rerotate else 0, p[5], width, p[6], _stream(stream))
     _check(st, "mla_cache_compact")
 
 

@@ -5,19 +5,23 @@
 // Every kept row that moves is read once and written once, and nothing is staged in
 // memory.  In place that is safe in this order: row j may be overwritten once every
 // reader of row j has read it, and its readers sit at positions j' <= j (keep_idx[j'] =
-// j >= j').  A CTA walks the positions upward in tiles, loads run ahead, and a tile is
-// written after a barrier that says that all reads of it and of the tiles below are
-// done; loads of later tiles touch rows that no write so far has reached.
+// j >= j').  A sequence's positions are walked upward in tiles, loads run ahead, and a
+// tile is written when all reads of it and of the tiles below are done; loads of later
+// tiles touch rows that no write so far has reached.
 //
-// Work is split by columns: a CTA takes one 128-byte slice of the row of one sequence
-// (nine slices of a 576-wide row), and the slices know nothing of each other.  With few
-// sequences, a cluster of CTAs shares a slice: each takes every cluster-size-th tile,
-// and the barrier becomes the cluster's.  One more slice per sequence moves the mass.
+// Bytes bind it: two row widths per moved row.  The parallel work comes from splitting
+// the rows into slices of columns, which know nothing of each other; with few sequences
+// also from a cluster of CTAs per slice, each taking every cluster-size-th tile.  The RoPE
+// part is cut into narrower slices than the latent: turning it costs more than moving
+// it.  The mass moves with the first slice.
 //
-// Bytes bind it: two row widths per moved row.  The copies are cp.async into a ring of
-// tiles that each thread fills and empties for itself (a thread writes out the pieces
-// that it loaded, so shared memory needs no barrier of its own), with the indices and
-// page ids of a tile fetched one tile earlier than its rows.
+// A CTA's threads go round by round, a tile each: start the copies of a later tile
+// (cp.async into a ring), wait until this round's tile has landed in all CTAs of the
+// cluster, write it.  A thread writes the 16-byte pieces that it loaded, the same of every
+// tile, so the ring needs no barrier of its own.  An index leads to two page ids and those to
+// the rows: each thread looks up one row of every kBatch tiles, and its three
+// dependent loads are a batch apart.  (One bulk copy per row, by one thread, was bound
+// by its issue, 40 ns each; roles in warps of their own, by the six hand-overs of a tile.)
 #include "common.cuh"
 #include "evict.h"
 #include "sm100.cuh"
@@ -28,199 +32,244 @@ namespace {
 
 using namespace sm100;
 
-constexpr int kThreads = 256;
-constexpr int kPieces = 4;                       // 16-byte pieces of a tile per thread
-constexpr int kTileBytes = kThreads * kPieces * 16;   // 16 KB: 128 rows of a 128-byte slice
-constexpr int kStages = 6;                       // ring of tiles: 96 KB, two CTAs per SM
-constexpr int kSliceVecs = 8;                    // 16-byte pieces of a row per slice
-constexpr int kTileRows = kThreads * kPieces / kSliceVecs;
-constexpr int kMassRows = 8;                     // mass values per thread and tile
-constexpr int kMaxCluster = 8;
+constexpr int kThreads = 512;
+constexpr int kPieces = 2;                       // 16-byte pieces of a tile per thread
+constexpr int kTilePieces = kThreads * kPieces;  // 16 KB
+constexpr int kAhead = 4;                        // rounds from the start of a tile's copies to its write
+constexpr int kStages = kAhead + 1;              // ring of tiles: 80 KB, two CTAs per SM
+constexpr int kBatch = 4;                        // tiles whose rows are looked up together
+constexpr int kMaxTileRows = kThreads / kBatch;
+constexpr int kMaxCluster = 16;
+constexpr int kMinVecs = 8, kMaxVecs = 64;       // 16-byte pieces of a latent slice
+static_assert(kAhead == kBatch, "a batch is looked up a batch before its first load");
 
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
-
 // (x, y) of a RoPE pair turned by delta positions; turn = 2^64 times the pair's
 // rotation per position as a fraction of a full turn.  delta * turn modulo 2^64 is the
-// whole rotation modulo one turn, exactly, so far moves keep their phase; its upper 32 bits
-// give the angle in [-pi, pi) to 2^-32 turns, and the hardware sine and cosine there are
-// good to 2^-21, against the 2^-9 of the bf16 result.
+// whole rotation modulo one turn, exactly, so far moves keep their phase.  Its upper 23
+// bits, rounded, become a float in [-1/2, 1/2) by their position in it (a conversion would go
+// to the unit of the sine and cosine, which is the busy one): an angle good to 2^-21.3 and
+// the hardware's sine and cosine, good to 2^-21.4, against the 2^-9 of the bf16 result.
 __device__ __forceinline__ uint32_t turn_pair(uint32_t xy, int delta, uint64_t turn) {
-  const int32_t phase = (int32_t)(((uint64_t)(int64_t)delta * turn) >> 32);
-  const float ang = (float)phase * 1.4629180792671596e-9f;   // 2 pi / 2^32
+  const uint32_t phase = (uint32_t)(((uint64_t)(int64_t)delta * turn) >> 32);
+  const float ang = (__uint_as_float(0x3F800000u | ((phase + 0x80000100u) >> 9)) - 1.5f) * 6.283185307f;
   const float c = __cosf(ang), s = __sinf(ang);
   const float x = bf16_lo(xy), y = bf16_hi(xy);
   return pack_bf16x2(x * c - y * s, x * s + y * c);
 }
 
-struct Seq {
-  int len, new_len;
-  const int32_t* idx;      // keep_idx of the sequence
-  const int32_t* pages;    // page table row
+struct Geometry {
+  int cluster;                     // CTAs that share a sequence's slice
+  int plain_vecs, plain_slices;    // 16-byte pieces of a slice of the columns that are only moved, and their slices
+  int turn_vecs, turn_slices;      // the same for the columns that are turned
+  int page_shift;                  // log2(page_size), or -1
 };
 
-// Row index of the pool for cache index n, or -1 (and a recorded range error) when
-// the page table names a page outside the pool.
-__device__ __forceinline__ int64_t pool_row(const CompactArgs& a, const Seq& q, int n, int shift) {
-  const int pg = shift >= 0 ? n >> shift : n / a.page_size;
-  const int id = q.pages[pg];
-  if (id < 0 || id >= a.num_pages) {
-    record_status(a.dev_status, MLA_ERR_RANGE);
-    return -1;
-  }
-  return (int64_t)id * a.page_size + (n - pg * a.page_size);
-}
+constexpr uint32_t kNone = 0xFFFFFFFFu;
 
-// The cache index that moves to position j, or -1 when nothing moves there: j past the
-// end, a row that stays, an index outside [j, len) (a recorded range error).
-__device__ __forceinline__ int source_of(const CompactArgs& a, const Seq& q, int j) {
-  if (j >= q.new_len) return -1;
-  const int n = q.idx[j];
-  if (n == j) return -1;
-  if (n < j || n >= q.len) {
-    record_status(a.dev_status, MLA_ERR_RANGE);
-    return -1;
-  }
-  return n;
-}
+struct CompactSmem {
+  uint4 ring[kStages][kThreads * kPieces];
+  // the rows of a tile, by batch: pool rows (kNone: the row stays) and the distance
+  // moved (0: neither row nor mass moves)
+  uint32_t src[2][kThreads];
+  uint32_t dst[3][kThreads];
+  int delta[3][kThreads];
+  float mass[kStages][kMaxTileRows];
+  uint64_t turn[kMaxRopePairs];
+};
 
-__global__ void __launch_bounds__(kThreads)
-cache_compact_kernel(const __grid_constant__ CompactArgs a, const int cluster, const int page_shift) {
-  extern __shared__ __align__(16) unsigned char ring[];
+__global__ void __launch_bounds__(kThreads, 2)
+cache_compact_kernel(const __grid_constant__ CompactArgs a, const __grid_constant__ Geometry geo) {
+  extern __shared__ __align__(128) unsigned char smem_raw[];
+  CompactSmem* sm = reinterpret_cast<CompactSmem*>(smem_raw);
+  const int cluster = geo.cluster, shift = geo.page_shift;
   const int tid = threadIdx.x;
   const int rank = (int)cluster_ctarank();
   const int slice = blockIdx.x / cluster;
   const int b = blockIdx.y;
-  const int rv = (a.d_c + a.d_rope) / 8;
-  const int slices = (rv + kSliceVecs - 1) / kSliceVecs;
-  auto sync = [&] {
-    if (cluster > 1) cluster_sync(); else __syncthreads();
-  };
+  const bool with_mass = a.mass != nullptr && slice == 0;
 
+  for (int i = tid; i < a.d_rope / 2; i += kThreads) sm->turn[i] = a.turn[i];
   grid_dependency_wait();
   allow_dependent_launch();
-  Seq q;
-  q.len = a.seq_lens[b];
-  q.new_len = a.new_lens[b];
-  q.idx = a.keep_idx + (size_t)b * a.keep_stride;
-  q.pages = a.page_table + (size_t)b * a.max_pages;
-  if (q.len < 0 || q.len > a.max_pages * a.page_size || q.new_len < 0 || q.new_len > q.len ||
-      q.new_len > a.keep_stride) {
+  const int len = a.seq_lens[b], new_len = a.new_lens[b];
+  if (len < 0 || len > a.max_pages * a.page_size || new_len < 0 || new_len > len || new_len > a.keep_stride) {
     if (blockIdx.x == 0 && tid == 0) record_status(a.dev_status, MLA_ERR_RANGE);
     return;                                    // the whole cluster
   }
 
-  if (slice == slices) {
-    // ---------------------------------------------------------------- attention mass
-    float* mass = a.mass + (size_t)b * a.mass_stride;
-    constexpr int kRows = kThreads * kMassRows;
-    const int rounds = (q.new_len + kRows * cluster - 1) / (kRows * cluster);
-    for (int r = 0; r < rounds; ++r) {
-      const int j0 = (r * cluster + rank) * kRows + tid;
-      int n[kMassRows];
-      float v[kMassRows];
+  // this slice: pieces [vec0, vec0 + n_vecs) of a row
+  const int vecs = (a.d_c + a.d_rope) / 8, latent = a.d_c / 8;
+  const int plain = a.rerotate ? latent : vecs;
+  const bool turns = slice >= geo.plain_slices;
+  const int vec0 = turns ? plain + (slice - geo.plain_slices) * geo.turn_vecs : slice * geo.plain_vecs;
+  const int n_vecs = turns ? min(geo.turn_vecs, vecs - vec0) : min(geo.plain_vecs, plain - vec0);
+  const int rows = min(kMaxTileRows, kThreads * kPieces / n_vecs);       // of a tile
+  const int64_t row_bytes = (int64_t)vecs * 16;
+  float* mass = with_mass ? a.mass + (size_t)b * a.mass_stride : nullptr;
+  const int rounds = (new_len + rows * cluster - 1) / (rows * cluster);
+
+  // this thread's pieces of every tile: the row within the tile and the place in the row
+  int row_of[kPieces];
+  char* pool_at[kPieces];
 #pragma unroll
-      for (int k = 0; k < kMassRows; ++k) n[k] = source_of(a, q, j0 + k * kThreads);
-#pragma unroll
-      for (int k = 0; k < kMassRows; ++k) v[k] = n[k] >= 0 ? *(volatile float*)(mass + n[k]) : 0.f;
-      sync();                                  // every value of this round has been read
-#pragma unroll
-      for (int k = 0; k < kMassRows; ++k)
-        if (n[k] >= 0) mass[j0 + k * kThreads] = v[k];
-    }
-    return;
+  for (int k = 0; k < kPieces; ++k) {
+    const int i = tid + k * kThreads;
+    row_of[k] = i < rows * n_vecs ? i / n_vecs : -1;
+    pool_at[k] = reinterpret_cast<char*>(a.pool) + (vec0 + i % n_vecs) * 16;
   }
+  const uint32_t ring0 = smem_u32(&sm->ring[0][tid]);
 
-  // ------------------------------------------------------------------ one slice of the rows
-  const int vec = slice * kSliceVecs + tid % kSliceVecs;   // this thread's 16-byte piece of the row
-  const bool live = vec < rv;
-  const int pair0 = a.rerotate ? (vec * 8 - a.d_c) / 2 : -1;   // its first RoPE pair
-  const bool turns = a.rerotate && vec * 8 >= a.d_c && live;
-  uint64_t turn[4] = {0, 0, 0, 0};
-  if (turns)
-#pragma unroll
-    for (int k = 0; k < 4; ++k) turn[k] = a.turn[pair0 + k];
-  const int row_in_tile = tid / kSliceVecs;
-  constexpr int kRowStep = kThreads / kSliceVecs;
-  char* pool = reinterpret_cast<char*>(a.pool);
-  const int64_t row_bytes = (int64_t)rv * 16;
-  const int rounds = (q.new_len + kTileRows * cluster - 1) / (kTileRows * cluster);
-  const uint32_t ring0 = smem_u32(ring) + tid * 16;
-  auto position = [&](int r, int k) { return (r * cluster + rank) * kTileRows + row_in_tile + k * kRowStep; };
-
-  // the piece of tile r goes to stage r % kStages; returns which of the pieces move
-  auto load = [&](int r) {
-    if (r < rounds && live) {
+  // the row that this thread looks up: row `row` of tile `kBatch * batch + tile`
+  const int tile = tid / kMaxTileRows, row = tid % kMaxTileRows;
+  const int32_t* idx = a.keep_idx + (size_t)b * a.keep_stride;
+  const int32_t* pages = a.page_table + (size_t)b * a.max_pages;
+  auto position = [&](int r, int i) { return (r * cluster + rank) * rows + i; };
+  auto index_of = [&](int batch) {             // j itself, which stays, where there is no such row
+    const int j = position(batch * kBatch + tile, row);
+    return row < rows && j < new_len ? __ldg(idx + j) : j;
+  };
+  auto page_of = [&](int n) { return __ldg(pages + (shift >= 0 ? n >> shift : n / a.page_size)); };
+  auto in_page = [&](int n) { return shift >= 0 ? n & (a.page_size - 1) : n % a.page_size; };
+  int n_next = index_of(0);                    // the next batch's index, and what was found with the
+  int j_now = 0, n_now = -1;                   // current one's: position, source index (-1: nothing
+  int src_page = 0, dst_page = 0;              // moves) and page ids
+  auto look_up = [&](int batch) {              // the pages of `batch`, the indices of the one after it
+    j_now = position(batch * kBatch + tile, row);
+    n_now = n_next;
+    if (n_now != j_now && (n_now < j_now || n_now >= len)) record_status(a.dev_status, MLA_ERR_RANGE);
+    if (n_now <= j_now || n_now >= len) n_now = -1;
+    if (n_now >= 0) {
+      src_page = page_of(n_now);
+      dst_page = page_of(j_now);
+    }
+    n_next = index_of(batch + 1);
+  };
+  auto resolve = [&](int batch) {
+    uint32_t src = kNone, dst = kNone;
+    if (n_now >= 0) {
+      if ((uint32_t)src_page < (uint32_t)a.num_pages && (uint32_t)dst_page < (uint32_t)a.num_pages) {
+        src = (uint32_t)src_page * a.page_size + in_page(n_now);
+        dst = (uint32_t)dst_page * a.page_size + in_page(j_now);
+      } else {
+        record_status(a.dev_status, MLA_ERR_RANGE);
+      }
+    }
+    sm->src[batch & 1][tid] = src;
+    sm->dst[batch % 3][tid] = dst;
+    sm->delta[batch % 3][tid] = n_now >= 0 ? j_now - n_now : 0;
+  };
+  auto load = [&](int r, int stage) {
+    if (r < rounds) {
+      const uint32_t* src_of = &sm->src[(r / kBatch) & 1][r % kBatch * kMaxTileRows];
 #pragma unroll
       for (int k = 0; k < kPieces; ++k) {
-        const int n = source_of(a, q, position(r, k));
-        if (n < 0) continue;
-        const int64_t row = pool_row(a, q, n, page_shift);
-        if (row < 0) continue;
-        cp_async16(ring0 + (r % kStages) * kTileBytes + k * kThreads * 16, pool + row * row_bytes + vec * 16);
+        if (row_of[k] < 0) continue;
+        const uint32_t src = src_of[row_of[k]];
+        if (src != kNone)
+          cp_async16(ring0 + stage * (kThreads * kPieces * 16) + k * (kThreads * 16), pool_at[k] + src * row_bytes);
+      }
+      if (with_mass && tid < rows) {
+        const int d = sm->delta[r / kBatch % 3][r % kBatch * kMaxTileRows + tid];
+        if (d != 0) cp_async4(smem_u32(&sm->mass[stage][tid]), mass + position(r, tid) - d);
       }
     }
     cp_async_commit();
   };
 
-  for (int r = 0; r < kStages - 1; ++r) load(r);
+  look_up(0);
+  resolve(0);
+  look_up(1);
+  resolve(1);
+  look_up(2);
+  __syncthreads();
+  for (int r = 0; r < kAhead; ++r) load(r, r);
+  int stage = 0;                               // r % kStages
   for (int r = 0; r < rounds; ++r) {
-    load(r + kStages - 1);
-    cp_async_wait<kStages - 1>();
-    sync();                                    // all reads of tiles <= r, in every CTA, are done
-    if (!live) continue;
+    load(r + kAhead, stage == 0 ? kStages - 1 : stage - 1);
+    cp_async_wait<kAhead>();                   // tile r is here
+    if (cluster > 1) {
+      __syncwarp();
+      cluster_arrive_relaxed();                // orders nothing: the copies have landed
+    }
+    if (r % kBatch == kBatch - 1) {
+      resolve(r / kBatch + 2);
+      look_up(r / kBatch + 3);
+      __syncthreads();
+    } else if (cluster == 1) {
+      __syncthreads();
+    }
+    if (cluster > 1) cluster_wait();           // all reads of tiles <= r, in every CTA, are done
+    const uint32_t* dst_of = &sm->dst[r / kBatch % 3][r % kBatch * kMaxTileRows];
+    const int* delta_of = &sm->delta[r / kBatch % 3][r % kBatch * kMaxTileRows];
 #pragma unroll
     for (int k = 0; k < kPieces; ++k) {
-      const int j = position(r, k);
-      const int n = source_of(a, q, j);
-      if (n < 0 || pool_row(a, q, n, page_shift) < 0) continue;
-      const int64_t row = pool_row(a, q, j, page_shift);
-      if (row < 0) continue;
-      uint4 u = *reinterpret_cast<const uint4*>(ring + (r % kStages) * kTileBytes + k * kThreads * 16 + tid * 16);
+      if (row_of[k] < 0) continue;
+      const uint32_t dst = dst_of[row_of[k]];
+      if (dst == kNone) continue;
+      uint4 u = sm->ring[stage][tid + k * kThreads];
       if (turns) {
-        const int delta = j - n;
-        u.x = turn_pair(u.x, delta, turn[0]);
-        u.y = turn_pair(u.y, delta, turn[1]);
-        u.z = turn_pair(u.z, delta, turn[2]);
-        u.w = turn_pair(u.w, delta, turn[3]);
+        const uint64_t* turn = sm->turn + (vec0 - latent + (tid + k * kThreads) % n_vecs) * 4;
+        const int d = delta_of[row_of[k]];
+        u.x = turn_pair(u.x, d, turn[0]);
+        u.y = turn_pair(u.y, d, turn[1]);
+        u.z = turn_pair(u.z, d, turn[2]);
+        u.w = turn_pair(u.w, d, turn[3]);
       }
-      *reinterpret_cast<uint4*>(pool + row * row_bytes + vec * 16) = u;
+      *reinterpret_cast<uint4*>(pool_at[k] + dst * row_bytes) = u;
     }
+    if (with_mass && tid < rows && delta_of[tid] != 0) mass[position(r, tid)] = sm->mass[stage][tid];
+    if (++stage == kStages) stage = 0;
   }
+  cp_async_wait<0>();
 }
 
 }  // namespace
 
 cudaError_t launch_cache_compact(const CompactArgs& a, int sms, cudaStream_t stream) {
-  const int rv = (a.d_c + a.d_rope) / 8;
-  const int slices = (rv + kSliceVecs - 1) / kSliceVecs;
-  // CTAs sharing a slice: as many as still give every CTA an SM
-  int cluster = 1;
-  while (cluster < kMaxCluster && (int64_t)2 * cluster * slices * a.batch <= sms) cluster *= 2;
-  int shift = -1;
+  const int vecs = (a.d_c + a.d_rope) / 8, plain = a.rerotate ? a.d_c / 8 : vecs, turned = vecs - plain;
+  Geometry geo;
+  // the widest slices (the longest pieces of a row) that give every SM a CTA; then clusters
+  // while two CTAs per SM hold them all
+  int64_t sets = 0;
+  for (geo.plain_vecs = kMaxVecs;; geo.plain_vecs /= 2) {
+    geo.turn_vecs = geo.plain_vecs / 4;
+    geo.plain_slices = (plain + geo.plain_vecs - 1) / geo.plain_vecs;
+    geo.turn_slices = (turned + geo.turn_vecs - 1) / geo.turn_vecs;
+    sets = (int64_t)(geo.plain_slices + geo.turn_slices) * a.batch;
+    if (sets >= sms || geo.plain_vecs == kMinVecs) break;
+  }
+  for (geo.cluster = 1; geo.cluster < kMaxCluster && 2 * geo.cluster * sets <= 2 * sms;) geo.cluster *= 2;
+  geo.page_shift = -1;
   if ((a.page_size & (a.page_size - 1)) == 0)
-    for (shift = 0; (1 << shift) < a.page_size; ++shift) {}
-  const int smem = kStages * kTileBytes;
+    for (geo.page_shift = 0; (1 << geo.page_shift) < a.page_size; ++geo.page_shift) {}
+  const int smem = (int)sizeof(CompactSmem);
   cudaError_t e = cudaFuncSetAttribute(cache_compact_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  e = cudaFuncSetAttribute(cache_compact_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = cluster;
+  attr[0].val.clusterDim.x = geo.cluster;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
   attr[1] = pdl_attribute();
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((slices + (a.mass != nullptr ? 1 : 0)) * cluster, a.batch, 1);
+  cfg.gridDim = dim3((geo.plain_slices + geo.turn_slices) * geo.cluster, a.batch, 1);
   cfg.blockDim = dim3(kThreads, 1, 1);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  e = cudaLaunchKernelEx(&cfg, cache_compact_kernel, a, cluster, shift);
+  e = cudaLaunchKernelEx(&cfg, cache_compact_kernel, a, geo);
   if (e != cudaSuccess) return e;
   return cudaGetLastError();
 }

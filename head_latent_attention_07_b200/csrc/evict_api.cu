@@ -114,6 +114,7 @@ int mla_cache_compact(const mla_dims* dims, mla_bf16* pool, const int32_t* page_
   if (st != MLA_OK) return st;
   if (keep_stride < 1 || (rerotate != 0 && rerotate != 1)) return MLA_ERR_INVALID_ARG;
   if ((st = check_cache_shape(dims, batch, max_pages, num_pages)) != MLA_OK) return st;
+  if ((int64_t)num_pages * dims->page_size >= UINT32_MAX) return MLA_ERR_UNSUPPORTED;   // row numbers are 32 bits
   if (!pool || !page_table || !seq_lens || !keep_idx || !new_lens) return MLA_ERR_INVALID_ARG;
   if (mass && mass_stride < (int64_t)max_pages * dims->page_size) return MLA_ERR_INVALID_ARG;
   if (!aligned16(pool) || !aligned16(page_table) || !aligned16(seq_lens) || !aligned16(keep_idx) ||
@@ -126,13 +127,13 @@ int mla_cache_compact(const mla_dims* dims, mla_bf16* pool, const int32_t* page_
   a.mass = mass; a.dev_status = dev_status; a.mass_stride = mass_stride; a.keep_stride = keep_stride;
   a.batch = batch; a.d_c = dims->d_c; a.d_rope = dims->d_rope; a.page_size = dims->page_size;
   a.max_pages = max_pages; a.num_pages = num_pages; a.rerotate = rerotate;
+  // the pairs' rotation per position in turns, theta^(-2i / d_rope) / (2 pi); whole turns
+  // change nothing, only the fraction counts
   const long double theta = dims->rope_theta > 0.f ? dims->rope_theta : 10000.f;
-  const long double two_pi = 6.283185307179586476925286766559L;
-  for (int i = 0; i < dims->d_rope / 2; ++i) {
-    // whole turns per position change nothing: only the fraction counts
-    const long double f = powl(theta, -2.0L * i / dims->d_rope) / two_pi;
+  const long double ratio = powl(theta, -2.0L / dims->d_rope);
+  long double f = 1.0L / 6.283185307179586476925286766559L;
+  for (int i = 0; i < dims->d_rope / 2; ++i, f *= ratio)
     a.turn[i] = (uint64_t)((f - floorl(f)) * 18446744073709551616.0L);
-  }
   return cuda_status(mla::launch_cache_compact(a, sms, (cudaStream_t)stream));
 }
 

@@ -424,7 +424,7 @@ int mla_evict_select(const float* mass, int64_t mass_stride, const int32_t* seq_
  * Rows with keep_idx[b][j] == j are not touched.  An index outside [j, seq_lens[b])
  * or a page outside the pool records MLA_ERR_RANGE and row j stays as it was; a
  * sequence whose lengths are out of range records it and is left alone.
- * batch <= 1024 (else MLA_ERR_UNSUPPORTED).
+ * batch <= 1024 and num_pages * page_size < 2^32 - 1 (else MLA_ERR_UNSUPPORTED).
  */
 int mla_cache_compact(const mla_dims* dims, mla_bf16* pool, const int32_t* page_table, const int32_t* seq_lens,
                       const int32_t* keep_idx, int64_t keep_stride, const int32_t* new_lens, int32_t batch,

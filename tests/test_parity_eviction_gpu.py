@@ -396,6 +396,15 @@ def test_compact_without_turning_and_without_mass():
     check_compact(Cache(lens, 1, 1, seed=4), [[], [], []])
 
 
+def test_compact_negative_index():
+    c = Cache([300], 1, 1, seed=7)
+    before = bits_of(c.pool)
+    M.mla_cache_compact(c.dims, c.pool, c.page_table, c.seq_lens, dev_i32([[0, -1, -2**31]]), dev_i32([3]), mass=c.mass,
+                        dev_status=c.status)
+    assert M.mla_status_read(c.status) == M.MLA_ERR_RANGE
+    assert np.array_equal(bits_of(c.pool), before) and np.array_equal(c.mass.cpu().numpy(), c.mass0)
+
+
 def test_compact_range_errors():
     c = Cache([300, 200, 100, 260], 1, 1, seed=6)
     before = bits_of(c.pool)
