@@ -4,16 +4,19 @@
 // A cluster of 1 to 8 CTAs takes one sequence, each CTA a contiguous part of it.
 // The mass values become unsigned keys in the same order (NaN above all, -0 equal
 // to +0) and are read from memory once, into shared memory.  The key of the last
-// token that stays is found by narrowing a key range: the range (at first from the
-// smallest to the largest key) is cut into 2048 bins, their counts are summed over
-// the cluster, and the bin that holds the wanted rank becomes the next range.
-// Each round divides the range by 2048, so at most three are needed, and most
-// selections end in the second with a bin that is kept whole.  Starting
-// from the keys' own range instead of their top bits spreads the masses, which
-// share a few exponents, over all bins: shared-memory atomics on one bin serialise.
-// Last, each warp counts what it keeps, and the counts before it (over warps and
-// lower CTAs) are its place in the ascending output; of the tokens equal to the
-// threshold the lowest indices stay.
+// token that stays is found by narrowing a key range: the range is cut into 2048 bins,
+// their counts are summed over the cluster, and the bin that holds the wanted rank
+// becomes the next range.  The first bins are 2^17 keys wide (64 to a factor of two)
+// over the values from 2^-24 to 2^8, where masses lie, and the outer two hold all
+// beyond: so the keys spread over many bins (shared-memory atomics on one bin
+// serialise), and the second round mostly ends it with a bin that is kept whole.  A later
+// round divides the range by 2048: four rounds at most.  Last, each warp counts what it
+// keeps, and the counts before it (over warps and lower CTAs) are its place in the
+// ascending output; of the tokens equal to the threshold the lowest indices stay.
+//
+// Latency binds it (2 MB of mass are read in well under a microsecond): one cluster
+// barrier a round, which the counts of groups of bins cross; the bins of the one group that
+// matters are read from the other CTAs' shared memory after it.
 #include "common.cuh"
 #include "evict.h"
 #include "sm100.cuh"
@@ -24,20 +27,19 @@ namespace {
 
 using namespace sm100;
 
-constexpr int kThreads = 1024;
-constexpr int kWarps = kThreads / 32;
-constexpr int kBins = 2048;
+constexpr int kMaxThreads = 1024;
+constexpr int kBins = 2048, kGroups = kBins / 32;
+constexpr int kFirstShift = 17;
+constexpr uint32_t kFirstLo = 0x80000000u | ((127u - 24u) << 23);   // key of 2^-24
 constexpr int kMaxCluster = 8;
-constexpr int kMaxStaged = 49152;      // keys of a CTA kept in shared memory (192 KB); later ones are read again
+constexpr int kMaxStaged = 40960;      // keys of a CTA kept in shared memory (160 KB); later ones are read again
 
 struct SelectSmem {
-  uint32_t hist[kBins];
-  uint32_t lo[kMaxCluster], hi[kMaxCluster];   // smallest and largest key of each CTA
-  uint32_t total[kMaxCluster];                 // a round's count in each CTA's share of the bins
-  uint32_t found[2];                           // the bin of the wanted rank, and the count above it within its share
-  uint32_t found_count;
+  uint32_t hist[2][kBins];                     // this CTA's counts; the rounds alternate
+  uint32_t coarse[kMaxCluster][kGroups];       // each CTA's counts in groups of 32 bins
   uint32_t kept[kMaxCluster], ties[kMaxCluster];
-  uint32_t warp_a[kWarps], warp_b[kWarps];
+  uint32_t warp_a[32], warp_b[32];
+  uint32_t found_bin, found_above, found_count;   // the bin of the wanted rank
 };
 
 // Unsigned key in the order of the value: larger mass, larger key.
@@ -65,21 +67,28 @@ __device__ __forceinline__ uint32_t warp_inclusive(uint32_t v, int lane) {
   return v;
 }
 
-__global__ void __launch_bounds__(kThreads, 1)
+// In a warp whose lanes hold counts from the top down: the lane in which the
+// `need`-th falls, and the count before it.
+__device__ __forceinline__ int lane_of_rank(uint32_t v, uint32_t need, int lane, uint32_t* before) {
+  const uint32_t incl = warp_inclusive(v, lane);
+  const int at = __ffs(__ballot_sync(0xffffffffu, incl >= need)) - 1;
+  *before = __shfl_sync(0xffffffffu, incl - v, at);
+  return at;
+}
+
+__global__ void __launch_bounds__(kMaxThreads, 1)
 evict_select_kernel(const SelectArgs a, const int cluster, const int staged_max) {
   extern __shared__ __align__(16) unsigned char smem_raw[];
   SelectSmem* sm = reinterpret_cast<SelectSmem*>(smem_raw);
   uint32_t* keys = reinterpret_cast<uint32_t*>(smem_raw + ((sizeof(SelectSmem) + 15) & ~size_t(15)));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int threads = blockDim.x, warps = threads >> 5;
   const int rank = (int)cluster_ctarank();
   const int b = blockIdx.x / cluster;
   auto sync = [&] {
     if (cluster > 1) cluster_sync(); else __syncthreads();
   };
-  // the same word of shared memory in every CTA of the cluster
-  auto tell_all = [&](uint32_t* where, uint32_t v) {
-    for (int r = 0; r < cluster; ++r) st_remote(mapa(smem_u32(where), r), v);
-  };
+  for (int i = tid; i < kBins; i += threads) sm->hist[0][i] = 0;
 
   grid_dependency_wait();
   allow_dependent_launch();
@@ -97,7 +106,7 @@ evict_select_kernel(const SelectArgs a, const int cluster, const int staged_max)
   if (rank == 0 && tid == 0) a.new_lens[b] = new_len;
   int32_t* out = a.keep_idx + (size_t)b * a.keep_stride;
   if (new_len == len) {
-    for (int i = rank * kThreads + tid; i < len; i += cluster * kThreads) out[i] = i;
+    for (int i = rank * threads + tid; i < len; i += cluster * threads) out[i] = i;
     return;
   }
   const int first = min(a.n_sink, new_len);              // [0, first) stay
@@ -111,88 +120,60 @@ evict_select_kernel(const SelectArgs a, const int cluster, const int staged_max)
   const float* mass = a.mass + (size_t)b * a.mass_stride;
   auto key_at = [&](int i) { return i - begin < staged ? keys[i - begin] : mass_key(mass[i]); };
 
-  uint32_t kmin = 0xFFFFFFFFu, kmax = 0;
-#pragma unroll 4
-  for (int i = begin + tid; i < end; i += kThreads) {
-    const uint32_t k = mass_key(mass[i]);
-    if (i - begin < staged) keys[i - begin] = k;
-    if (i >= first && i < last) {
-      kmin = min(kmin, k);
-      kmax = max(kmax, k);
-    }
-  }
-  kmin = __reduce_min_sync(0xffffffffu, kmin);
-  kmax = __reduce_max_sync(0xffffffffu, kmax);
-  if (lane == 0) { sm->warp_a[warp] = kmin; sm->warp_b[warp] = kmax; }
-  for (int i = tid; i < kBins; i += kThreads) sm->hist[i] = 0;
-  // a CTA of the cluster must have started before its shared memory is written
-  sync();
-  if (warp == 0) {
-    kmin = __reduce_min_sync(0xffffffffu, sm->warp_a[lane]);
-    kmax = __reduce_max_sync(0xffffffffu, sm->warp_b[lane]);
-    if (lane == 0) {
-      tell_all(&sm->lo[rank], kmin);
-      tell_all(&sm->hi[rank], kmax);
-    }
-  }
-  sync();
-  uint32_t lo = 0xFFFFFFFFu, hi = 0;
-  for (int r = 0; r < cluster; ++r) {
-    lo = min(lo, sm->lo[r]);
-    hi = max(hi, sm->hi[r]);
-  }
+#pragma unroll 8
+  for (int i = begin + tid; i < begin + staged; i += threads) keys[i - begin] = mass_key(mass[i]);
+  __syncthreads();
 
   // narrow [lo, hi] to the key of the last token that stays; `need` of the tokens in
   // it stay, and `whole` says that all of them do
   bool whole = false;
-  const int share = kBins / cluster;                     // bins summed by each CTA
-  while (need > 0 && !whole && lo < hi) {
-    int shift = 0;
-    while (((hi - lo) >> shift) >= (uint32_t)kBins) ++shift;
-    for (int i = max(begin, first) + tid; i < min(end, last); i += kThreads) {
+  uint32_t lo = 0, hi = 0xFFFFFFFFu;
+  for (int round = 0; need > 0 && !whole && lo < hi; ++round) {
+    // bin i holds the keys from base + (i << shift) on, the first and the last all beyond
+    const int shift = round == 0 ? kFirstShift : max(0, 21 - __clz(hi - lo));   // (hi - lo) >> shift < kBins
+    const uint32_t base = round == 0 ? kFirstLo : lo;
+    uint32_t* hist = sm->hist[round & 1];
+#pragma unroll 4
+    for (int i = max(begin, first) + tid; i < min(end, last); i += threads) {
       const uint32_t k = key_at(i);
-      if (k >= lo && k <= hi) atomicAdd(&sm->hist[(k - lo) >> shift], 1u);
+      if (k >= lo && k <= hi) atomicAdd(&hist[k < base ? 0 : min((k - base) >> shift, kBins - 1u)], 1u);
     }
-    sync();
-    // CTA r sums bins [r * share, (r + 1) * share) of all CTAs, two per thread at most,
-    // and scans its sums from the top bin down
-    uint32_t mine[2] = {0, 0};
-    const int top = (rank + 1) * share - 1;              // thread t holds bins top - 2t, top - 2t - 1
-#pragma unroll
-    for (int e = 0; e < 2; ++e)
-      if (2 * tid + e < share)
-        for (int r = 0; r < cluster; ++r) mine[e] += ld_remote(mapa(smem_u32(&sm->hist[top - 2 * tid - e]), r));
-    const uint32_t incl = warp_inclusive(mine[0] + mine[1], lane);
-    if (lane == 31) sm->warp_a[warp] = incl;
     __syncthreads();
-    uint32_t before = 0, all = 0;
-    for (int w = 0; w < kWarps; ++w) {
-      const uint32_t t = sm->warp_a[w];
-      if (w < warp) before += t;
-      all += t;
+    for (int g = warp; g < kGroups; g += warps) {
+      const uint32_t v = __reduce_add_sync(0xffffffffu, hist[g * 32 + lane]);
+      if (lane < cluster) st_remote(mapa(smem_u32(&sm->coarse[rank][g]), lane), v);
     }
-    before += incl - mine[0] - mine[1];                  // count in this share above this thread's bins
-    if (tid == 0) tell_all(&sm->total[rank], all);
     sync();
-    // the counts are read: clear them for the next round
-    for (int i = tid; i < kBins; i += kThreads) sm->hist[i] = 0;
-    uint32_t above = 0;                                  // count in the shares above this one
-    for (int r = rank + 1; r < cluster; ++r) above += sm->total[r];
-    above += before;
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      if (mine[e] > 0 && above < need && need <= above + mine[e]) {
-        tell_all(&sm->found[0], (uint32_t)(top - 2 * tid - e));
-        tell_all(&sm->found[1], above);
-        tell_all(&sm->found_count, mine[e]);
+    // the other counts were read before this barrier
+    for (int i = tid; i < kBins; i += threads) sm->hist[(round + 1) & 1][i] = 0;
+    if (warp == 0) {
+      // from the top: the pair of groups, the group, then the bin with the wanted rank
+      uint32_t c[2] = {0, 0}, v = 0, above, in_pair, in_group;
+      for (int r = 0; r < cluster; ++r) {
+        c[0] += sm->coarse[r][kGroups - 1 - 2 * lane];
+        c[1] += sm->coarse[r][kGroups - 2 - 2 * lane];
       }
-      above += mine[e];
+      const int pair = lane_of_rank(c[0] + c[1], need, lane, &above);
+      in_pair = __shfl_sync(0xffffffffu, c[0], pair);
+      const bool second = above + in_pair < need;
+      if (second) above += in_pair;
+      const int bin0 = (kGroups - 1 - 2 * pair - (second ? 1 : 0)) * 32;
+#pragma unroll
+      for (int r = 0; r < kMaxCluster; ++r)
+        if (r < cluster) v += ld_remote(mapa(smem_u32(&hist[bin0 + 31 - lane]), r));
+      const int at = lane_of_rank(v, need - above, lane, &in_group);
+      if (lane == at) {
+        sm->found_bin = bin0 + 31 - at;
+        sm->found_above = above + in_group;
+        sm->found_count = v;
+      }
     }
-    sync();
-    need -= sm->found[1];
+    __syncthreads();
+    need -= sm->found_above;
     whole = need == sm->found_count;
-    lo += sm->found[0] << shift;                         // stays at or below hi
-    hi = lo + min(hi - lo, (1u << shift) - 1u);
+    const uint32_t bin = sm->found_bin, from = base + (bin << shift);
+    if (bin < kBins - 1u) hi = from + min(hi - from, (1u << shift) - 1u);
+    if (bin > 0) lo = from;
   }
   // keys above hi stay; of those in [lo, hi]: all when `whole`, else (lo == hi) the
   // first `need`
@@ -209,41 +190,54 @@ evict_select_kernel(const SelectArgs a, const int cluster, const int staged_max)
   };
 
   // each warp's place: counts of the lower ranks, then of the lower warps
-  const int per_warp = ((end - begin + kWarps - 1) / kWarps + 31) & ~31;
+  const int per_warp = ((end - begin + warps - 1) / warps + 31) & ~31;
   const int wb = min(begin + warp * per_warp, end), we = min(wb + per_warp, end);
   uint32_t n_stay = 0, n_tie = 0;
-  for (int i = wb; i < we; i += 32) {
-    bool stays, tie;
-    classify(i + lane, &stays, &tie);
-    n_stay += __popc(__ballot_sync(0xffffffffu, stays));
-    n_tie += __popc(__ballot_sync(0xffffffffu, tie));
-  }
-  __syncthreads();                                       // warp_a of the last round has been read
-  if (lane == 0) { sm->warp_a[warp] = n_stay; sm->warp_b[warp] = n_tie; }
-  __syncthreads();
-  uint32_t stay0 = 0, tie0 = 0, stay_all = 0, tie_all = 0;
-  for (int w = 0; w < kWarps; ++w) {
-    const uint32_t s = sm->warp_a[w], t = sm->warp_b[w];
-    if (w < warp) { stay0 += s; tie0 += t; }
-    stay_all += s;
-    tie_all += t;
-  }
-  if (tid == 0) {
-    tell_all(&sm->kept[rank], stay_all);
-    tell_all(&sm->ties[rank], tie_all);
-  }
-  sync();
-  for (int r = 0; r < rank; ++r) {
-    stay0 += sm->kept[r];
-    tie0 += sm->ties[r];
-  }
+  uint32_t my_stay = 0, my_tie = 0;                      // lane l: the ballots of the warp's l-th group
+#pragma unroll 4
   for (int i = wb; i < we; i += 32) {
     bool stays, tie;
     classify(i + lane, &stays, &tie);
     const uint32_t sb = __ballot_sync(0xffffffffu, stays), tb = __ballot_sync(0xffffffffu, tie);
-    const uint32_t below = (1u << lane) - 1u;
+    if (i - wb == lane * 32) { my_stay = sb; my_tie = tb; }
+    n_stay += __popc(sb);
+    n_tie += __popc(tb);
+  }
+  if (lane == 0) { sm->warp_a[warp] = n_stay; sm->warp_b[warp] = n_tie; }
+  __syncthreads();
+  const uint32_t s = warp_inclusive(lane < warps ? sm->warp_a[lane] : 0, lane);
+  const uint32_t t = warp_inclusive(lane < warps ? sm->warp_b[lane] : 0, lane);
+  uint32_t stay0 = __shfl_sync(0xffffffffu, s, warp) - n_stay;
+  uint32_t tie0 = __shfl_sync(0xffffffffu, t, warp) - n_tie;
+  if (cluster > 1) {
+    if (warp == 0) {
+      const uint32_t stay_all = __shfl_sync(0xffffffffu, s, 31), tie_all = __shfl_sync(0xffffffffu, t, 31);
+      if (lane < cluster) {
+        st_remote(mapa(smem_u32(&sm->kept[rank]), lane), stay_all);
+        st_remote(mapa(smem_u32(&sm->ties[rank]), lane), tie_all);
+      }
+    }
+    sync();
+    for (int r = 0; r < rank; ++r) {
+      stay0 += sm->kept[r];
+      tie0 += sm->ties[r];
+    }
+  }
+  const uint32_t below = (1u << lane) - 1u;
+#pragma unroll 4
+  for (int i = wb; i < we; i += 32) {
+    uint32_t sb, tb;
+    if (i - wb < 32 * 32) {
+      sb = __shfl_sync(0xffffffffu, my_stay, (i - wb) >> 5);
+      tb = __shfl_sync(0xffffffffu, my_tie, (i - wb) >> 5);
+    } else {
+      bool stays, tie;
+      classify(i + lane, &stays, &tie);
+      sb = __ballot_sync(0xffffffffu, stays);
+      tb = __ballot_sync(0xffffffffu, tie);
+    }
     const uint32_t ties_before = tie0 + __popc(tb & below);
-    if (stays || (tie && ties_before < need))
+    if ((sb >> lane & 1u) || ((tb >> lane & 1u) && ties_before < need))
       out[stay0 + __popc(sb & below) + min(ties_before, need)] = i + lane;
     stay0 += __popc(sb);
     tie0 += __popc(tb);
@@ -253,11 +247,15 @@ evict_select_kernel(const SelectArgs a, const int cluster, const int staged_max)
 }  // namespace
 
 cudaError_t launch_evict_select(const SelectArgs& a, int sms, cudaStream_t stream) {
-  // CTAs per sequence: as many as give each about 2048 tokens, while all fit the GPU
+  // CTAs per sequence: as many as give each about 2048 tokens, while all fit the GPU.
+  // 64 sequences of up to 65536 took 71, 32 and 40 us with clusters of 1, 2 and 4 of 1024
+  // threads; 16 of 32768 took 13.6 and 14.7 us with 4 of 1024 and 8 of 512.
   int cluster = 1;
   while (cluster < kMaxCluster && (int64_t)2 * cluster * a.batch <= sms && a.mass_stride > (int64_t)2048 * cluster)
     cluster *= 2;
   const int64_t part = ((a.mass_stride + cluster - 1) / cluster + 31) & ~int64_t(31);
+  int threads = 512;
+  while (threads < kMaxThreads && threads * 8 < part) threads *= 2;
   const int staged = (int)(part < kMaxStaged ? part : kMaxStaged);
   const int smem = (int)((sizeof(SelectSmem) + 15) & ~size_t(15)) + staged * 4;
   cudaError_t e = cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
@@ -270,7 +268,7 @@ cudaError_t launch_evict_select(const SelectArgs& a, int sms, cudaStream_t strea
   attr[1] = pdl_attribute();
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(a.batch * cluster, 1, 1);
-  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.blockDim = dim3(threads, 1, 1);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cfg.attrs = attr;
