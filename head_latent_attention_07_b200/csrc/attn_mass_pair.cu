@@ -216,23 +216,33 @@ attn_mass_pair_kernel(const __grid_constant__ CUtensorMap tq, const __grid_const
     const uint32_t qfull0 = mapa(smem_u32(&bar->q_full[0]), 0);
     const int oob_row = a.num_pages * 64;        // a box starting here lies outside the pool: zero fill
     const uint64_t once = l2_policy_evict_first();
+    // the ids of this CTA's two pages of a tile are fetched while the tile before is loaded
     Cursor cur(prm, bar, share);
-    Item it;
+    Item next;
+    int next_id[2] = {0, 0};
+    auto fetch = [&]() -> bool {
+      if (!cur.next(&next)) return false;
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int pg = next.tile * 4 + (int)c * 2 + j;
+        if (pg * 64 < next.len) next_id[j] = __ldg(a.page_table + (size_t)next.b * a.max_pages + pg);
+      }
+      return true;
+    };
     int k = 0, gi = -1;                          // stages used, groups begun
-    bool ok = true;
-    while (ok && cur.next(&it)) {
+    bool ok = true, more = fetch();
+    while (ok && more) {
+      const Item it = next;
       if (it.first) ++gi;
       int y[2];
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        const int pg = it.tile * 4 + (int)c * 2 + j;
-        y[j] = oob_row;
-        if (pg * 64 < it.len) {
-          const int id = a.page_table[(size_t)it.b * a.max_pages + pg];
-          if (id >= 0 && id < a.num_pages) y[j] = id * 64;
-          else if (lane == 0) record_status(status, MLA_ERR_RANGE);
-        }
+        const bool in_seq = (it.tile * 4 + (int)c * 2 + j) * 64 < it.len;
+        const bool in_pool = next_id[j] >= 0 && next_id[j] < a.num_pages;
+        y[j] = in_seq && in_pool ? next_id[j] * 64 : oob_row;
+        if (in_seq && !in_pool && lane == 0) record_status(status, MLA_ERR_RANGE);
       }
+      more = fetch();
       const int qrow = it.b * prm.rows_total + it.group * NT + (int)c * (NT / 2);
       for (int blk = 0; blk < kBlocks; ++blk, ++k) {
         if (it.first) {
