@@ -9,21 +9,24 @@
 //
 //   tile    256 keys of a sequence (4 pages), 128 per CTA of the pair
 //   group   NT query rows (128 or 256), half of them in each CTA's shared memory
-// The keys stream: blocks of [128 keys x 64 columns] (16 KB) go by TMA through a ring,
-// and each is done with after its four MMAs.  A group's query stays in shared memory
-// (9 blocks) for as many tiles as possible; where a sequence has more than one group
-// (nq * H > 256), the worker takes kSubTiles tiles at a time through all groups, so that the
-// groups after the first find the keys in L2.  A query block is reloaded as soon as the
-// last tile of its group is through with that block.
-//
-// With one group the bound is HBM: 1152 bytes per key against 256 x NT x 576 products per
-// tile, about 4600 cycles of the tensor pipe at NT = 256 for 295 KB per pair, which takes
-// 6700 at the pair's share of the bandwidth.  With many groups the tensor pipe is.
+// One of the two stays in shared memory (9 blocks of 64 columns) while the other goes by
+// TMA through a ring of blocks, each done with after its four MMAs; a resident block is
+// reloaded as soon as its last MMAs are through.
+//   one group   (nq * H <= 256: decode) the group stays, the keys stream: HBM binds, 295 KB
+//               per tile and pair, 6700 cycles at the pair's share of the bandwidth, against
+//               4600 of the tensor pipe at NT = 256
+//   few groups  the same, the worker taking kSubTiles tiles at a time through all groups,
+//               so that the groups after the first find the keys in L2
+//   many groups the tile stays and the groups stream.  Both forms are bound by what an SM
+//               takes in from L2 (about 30 B/clk against the 32 that the tensor pipe would
+//               use): per group and tile 147 + 147 / 4 KB with the group resident, 147 + 147 /
+//               groups with the tile resident, so the tile is from more than 4 groups on.
 //
 // TMEM: two accumulators of NT columns, so that the sum over one tile runs beside the
 // next tile's MMAs.  Warps (256 threads): 0 loads (TMA), 1 owns TMEM and, in CTA 0, issues
-// the MMAs, 2 brings the groups' lse, 4-7 sum (warp w reads TMEM lanes 32 (w & 3) and on).  Every mbarrier wait is
-// bounded: on time-out the kernel records MLA_ERR_TIMEOUT, drains its MMAs and ends.
+// the MMAs, 2 brings the groups' lse, 4-7 sum (warp w reads TMEM lanes 32 (w & 3) and
+// on).  Every mbarrier wait is bounded: on time-out the kernel records MLA_ERR_TIMEOUT,
+// drains its MMAs and ends.
 #include <cuda.h>
 
 #include "common.cuh"
@@ -44,22 +47,27 @@ constexpr int kKeyBytes = 128 * 128;             // [128 keys x 64 columns] bf16
 constexpr int kSubTiles = 4;                     // tiles per pass over the groups: 74 pairs hold 87 MB of keys in L2
 constexpr long long kDrainCycles = 1ll << 24;
 
-template <int NT>
+// kKeys: the tile is resident and the groups stream, else the other way round
+template <int NT, bool kKeys>
 struct Layout {
-  static constexpr int kQBytes = NT / 2 * 128;                       // one block of this CTA's half of the group
+  static constexpr int kQueryBytes = NT / 2 * 128;                   // one block of this CTA's half of the group
+  static constexpr int kResBytes = kKeys ? kKeyBytes : kQueryBytes;  // a block of the resident operand
+  static constexpr int kRingBytes = kKeys ? kQueryBytes : kKeyBytes; // ... of the streaming one
   static constexpr int kStages = NT == 256 ? 5 : 9;
-  static constexpr int kOffK = kBlocks * kQBytes;
-  static constexpr int kOffLse = kOffK + kStages * kKeyBytes;        // fp32 [NT], log2 units
+  static constexpr int kOffRing = kBlocks * kResBytes;
+  static constexpr int kOffLse = kOffRing + kStages * kRingBytes;    // fp32 [NT], log2 units
   static constexpr int kOffBar = kOffLse + NT * 4;
   static constexpr int kBytes = kOffBar + 512 + 1024;                // + 1 KB alignment slack
 };
-static_assert(Layout<256>::kBytes <= 232448 && Layout<128>::kBytes <= 232448, "shared memory budget");
+static_assert(Layout<256, false>::kBytes <= 232448 && Layout<128, false>::kBytes <= 232448 &&
+                  Layout<256, true>::kBytes <= 232448,
+              "shared memory budget");
 
 struct Bars {
-  uint64_t k_full[9];    // CTA 0: both CTAs' key blocks landed in the stage (2 arrivals + bytes)
-  uint64_t k_empty[9];   // both: the MMAs are done with the stage
-  uint64_t q_full[9];    // CTA 0: both CTAs' halves of a query block landed
-  uint64_t q_empty[9];   // both: the group's MMAs are done with the query block
+  uint64_t ring_full[9]; // CTA 0: both CTAs' blocks landed in the stage (2 arrivals + bytes)
+  uint64_t ring_empty[9];// both: the MMAs are done with the stage
+  uint64_t res_full[9];  // CTA 0: both CTAs' blocks of the resident operand landed
+  uint64_t res_empty[9]; // both: the MMAs are done with that block
   uint64_t acc_full[2];  // both: a tile's scores are in TMEM
   uint64_t acc_empty[2]; // CTA 0: the 8 summing warps of the pair have read them
   uint64_t lse_full;     // local: a group's lse is in shared memory
@@ -88,36 +96,45 @@ __device__ __forceinline__ int seq_tiles(const MassArgs& a, int b, int* len) {
 // One accumulator's worth of work; every role walks the same ones in the same order.
 struct Item {
   int b, len, tile, group;
-  bool first, last;      // of the tiles that see this group's query in shared memory
+  bool first, last;      // with what is resident
 };
+template <bool kKeys>
 struct Cursor {
   const PairMassParams& p;
   int b, tile, left;     // next sequence and tile, tiles left of this worker's share
   int len = 0, sub0 = 0, sub1 = 0, t = 0, g = 0;
   __device__ Cursor(const PairMassParams& p_, const Bars* bar, int share) : p(p_), b(bar->b0), tile(bar->tile0), left(share) {}
   __device__ bool next(Item* it) {
-    if (t == sub1) {                             // the group's tiles are done
-      ++g;
-      if (g >= p.groups || sub1 == 0) {
-        if (left == 0) return false;
-        int n;
-        while (tile >= (n = seq_tiles(p.m, b, &len))) { ++b; tile = 0; }
-        sub0 = tile;
-        sub1 = min(n, tile + left);
-        if (p.groups > 1) sub1 = min(sub1, tile + kSubTiles);
-        left -= sub1 - sub0;
-        tile = sub1;
-        g = 0;
-      }
+    // through the groups of a tile (kKeys), or through the tiles [sub0, sub1) of a group
+    bool done;
+    if (kKeys) {
+      done = sub1 == 0 || ++g == p.groups;
+    } else if ((done = t == sub1)) {
       t = sub0;
+      done = ++g >= p.groups || sub1 == 0;
+    }
+    if (done) {
+      if (left == 0) return false;
+      int n;
+      while (tile >= (n = seq_tiles(p.m, b, &len))) { ++b; tile = 0; }
+      sub0 = t = tile;
+      sub1 = kKeys ? tile + 1 : min(n, tile + left);
+      if (!kKeys && p.groups > 1) sub1 = min(sub1, tile + kSubTiles);
+      left -= sub1 - sub0;
+      tile = sub1;
+      g = 0;
     }
     it->b = b;
     it->len = len;
     it->tile = t;
     it->group = g;
-    it->first = t == sub0;
-    ++t;
-    it->last = t == sub1;
+    if (kKeys) {
+      it->first = g == 0;
+      it->last = g == p.groups - 1;
+    } else {
+      it->first = t == sub0;
+      it->last = ++t == sub1;
+    }
     return true;
   }
 };
@@ -128,11 +145,11 @@ __device__ __forceinline__ bool elect_one() {
   return is_leader != 0;
 }
 
-template <int NT>
+template <int NT, bool kKeys>
 __global__ void __launch_bounds__(kThreads, 1)
 attn_mass_pair_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tp,
                       const __grid_constant__ PairMassParams prm) {
-  using L = Layout<NT>;
+  using L = Layout<NT, kKeys>;
   extern __shared__ unsigned char smem_raw[];
   unsigned char* sm =
       reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -149,10 +166,10 @@ attn_mass_pair_kernel(const __grid_constant__ CUtensorMap tq, const __grid_const
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < 9; ++s) {
-      mbar_init(&bar->k_full[s], 2);
-      mbar_init(&bar->k_empty[s], 1);
-      mbar_init(&bar->q_full[s], 2);
-      mbar_init(&bar->q_empty[s], 1);
+      mbar_init(&bar->ring_full[s], 2);
+      mbar_init(&bar->ring_empty[s], 1);
+      mbar_init(&bar->res_full[s], 2);
+      mbar_init(&bar->res_empty[s], 1);
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(&bar->acc_full[s], 1);
@@ -212,12 +229,12 @@ attn_mass_pair_kernel(const __grid_constant__ CUtensorMap tq, const __grid_const
 
   if (warp == 0) {
     // ------------------------------------------------------------ queries and keys (TMA)
-    const uint32_t kfull0 = mapa(smem_u32(&bar->k_full[0]), 0);
-    const uint32_t qfull0 = mapa(smem_u32(&bar->q_full[0]), 0);
+    const uint32_t ring_full0 = mapa(smem_u32(&bar->ring_full[0]), 0);
+    const uint32_t res_full0 = mapa(smem_u32(&bar->res_full[0]), 0);
     const int oob_row = a.num_pages * 64;        // a box starting here lies outside the pool: zero fill
     const uint64_t once = l2_policy_evict_first();
     // the ids of this CTA's two pages of a tile are fetched while the tile before is loaded
-    Cursor cur(prm, bar, share);
+    Cursor<kKeys> cur(prm, bar, share);
     Item next;
     int next_id[2] = {0, 0};
     auto fetch = [&]() -> bool {
@@ -229,11 +246,11 @@ attn_mass_pair_kernel(const __grid_constant__ CUtensorMap tq, const __grid_const
       }
       return true;
     };
-    int k = 0, gi = -1;                          // stages used, groups begun
+    int k = 0, ri = -1;                          // stages used, resident operands begun
     bool ok = true, more = fetch();
     while (ok && more) {
       const Item it = next;
-      if (it.first) ++gi;
+      if (it.first) ++ri;
       int y[2];
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
@@ -244,26 +261,35 @@ attn_mass_pair_kernel(const __grid_constant__ CUtensorMap tq, const __grid_const
       }
       more = fetch();
       const int qrow = it.b * prm.rows_total + it.group * NT + (int)c * (NT / 2);
+      auto load_keys = [&](unsigned char* dst, int blk, uint32_t full) {
+        mbar_arrive_expect_tx_cluster(full, kKeyBytes);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          if (prm.groups == 1)
+            tma_load_2d_pair_hint(dst + j * (kKeyBytes / 2), &tp, 64 * blk, y[j], full, once);
+          else
+            tma_load_2d_pair(dst + j * (kKeyBytes / 2), &tp, 64 * blk, y[j], full);
+        }
+      };
+      auto load_query = [&](unsigned char* dst, int blk, uint32_t full) {
+        mbar_arrive_expect_tx_cluster(full, L::kQueryBytes);
+        tma_load_2d_pair(dst, &tq, 64 * blk, qrow, full);
+      };
       for (int blk = 0; blk < kBlocks; ++blk, ++k) {
         if (it.first) {
-          if (gi > 0 && !(ok = wwait(&bar->q_empty[blk], (gi - 1) & 1))) break;
+          if (ri > 0 && !(ok = wwait(&bar->res_empty[blk], (ri - 1) & 1))) break;
+          unsigned char* dst = sm + blk * L::kResBytes;
           if (lane == 0) {
-            mbar_arrive_expect_tx_cluster(qfull0 + 8 * blk, L::kQBytes);
-            tma_load_2d_pair(sm + blk * L::kQBytes, &tq, 64 * blk, qrow, qfull0 + 8 * blk);
+            if (kKeys) load_keys(dst, blk, res_full0 + 8 * blk);
+            else load_query(dst, blk, res_full0 + 8 * blk);
           }
         }
         const int s = k % L::kStages;
-        if (k >= L::kStages && !(ok = wwait(&bar->k_empty[s], (k / L::kStages - 1) & 1))) break;
+        if (k >= L::kStages && !(ok = wwait(&bar->ring_empty[s], (k / L::kStages - 1) & 1))) break;
+        unsigned char* dst = sm + L::kOffRing + s * L::kRingBytes;
         if (lane == 0) {
-          unsigned char* dst = sm + L::kOffK + s * kKeyBytes;
-          mbar_arrive_expect_tx_cluster(kfull0 + 8 * s, kKeyBytes);
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            if (prm.groups == 1)
-              tma_load_2d_pair_hint(dst + j * (kKeyBytes / 2), &tp, 64 * blk, y[j], kfull0 + 8 * s, once);
-            else
-              tma_load_2d_pair(dst + j * (kKeyBytes / 2), &tp, 64 * blk, y[j], kfull0 + 8 * s);
-          }
+          if (kKeys) load_query(dst, blk, ring_full0 + 8 * s);
+          else load_keys(dst, blk, ring_full0 + 8 * s);
         }
         __syncwarp();
       }
@@ -272,29 +298,30 @@ attn_mass_pair_kernel(const __grid_constant__ CUtensorMap tq, const __grid_const
     // ------------------------------------------------------------ MMA issuer (CTA 0)
     if (c == 0) {
       const uint32_t idesc = idesc_bf16_f32(256, NT, 0, 0);
-      const uint32_t qa = smem_u32(sm), ka = smem_u32(sm + L::kOffK);
-      Cursor cur(prm, bar, share);
+      const uint32_t res = smem_u32(sm), ring = smem_u32(sm + L::kOffRing);
+      Cursor<kKeys> cur(prm, bar, share);
       Item it;
-      int k = 0, gi = -1, t = 0;
+      int k = 0, ri = -1, t = 0;
       bool ok = true;
       while (ok && cur.next(&it)) {
-        if (it.first) ++gi;
+        if (it.first) ++ri;
         if (t >= 2 && !wwait(&bar->acc_empty[t & 1], ((t >> 1) - 1) & 1)) break;
         const uint32_t d = tmem + (t & 1) * NT;
         for (int blk = 0; blk < kBlocks; ++blk, ++k) {
           const int s = k % L::kStages;
-          if (it.first && !(ok = wwait(&bar->q_full[blk], gi & 1))) break;
-          if (!(ok = wwait(&bar->k_full[s], (k / L::kStages) & 1))) break;
+          if (it.first && !(ok = wwait(&bar->res_full[blk], ri & 1))) break;
+          if (!(ok = wwait(&bar->ring_full[s], (k / L::kStages) & 1))) break;
           tc_fence_after();
           if (elect_one()) {
+            const uint32_t res_blk = res + blk * L::kResBytes, ring_blk = ring + s * L::kRingBytes;
 #pragma unroll
             for (int ks = 0; ks < 4; ++ks) {
-              const uint64_t da = smem_desc(ka + s * kKeyBytes + ks * 32, 16, 1024, kSwizzle128);
-              const uint64_t db = smem_desc(qa + blk * L::kQBytes + ks * 32, 16, 1024, kSwizzle128);
+              const uint64_t da = smem_desc((kKeys ? res_blk : ring_blk) + ks * 32, 16, 1024, kSwizzle128);
+              const uint64_t db = smem_desc((kKeys ? ring_blk : res_blk) + ks * 32, 16, 1024, kSwizzle128);
               mma_bf16_pair(d, da, db, idesc, blk + ks > 0 ? 1u : 0u);
             }
-            mma_commit_pair(&bar->k_empty[s]);
-            if (it.last) mma_commit_pair(&bar->q_empty[blk]);
+            mma_commit_pair(&bar->ring_empty[s]);
+            if (it.last) mma_commit_pair(&bar->res_empty[blk]);
             if (blk == kBlocks - 1) mma_commit_pair(&bar->acc_full[t & 1]);
           }
           __syncwarp();
@@ -309,11 +336,11 @@ attn_mass_pair_kernel(const __grid_constant__ CUtensorMap tq, const __grid_const
     __syncwarp();
   } else if (warp == 2) {
     // ------------------------------------------------------------ lse of a group's query rows
-    Cursor cur(prm, bar, share);
+    Cursor<kKeys> cur(prm, bar, share);
     Item it;
     int gi = 0;
     while (cur.next(&it)) {
-      if (!it.first) continue;
+      if (!kKeys && !it.first) continue;         // the same group still
       const int cols = prm.rows_total - it.group * NT;
       const float* src = a.lse + (size_t)it.b * prm.rows_total + it.group * NT;
       float l[NT / 32];
@@ -334,25 +361,28 @@ attn_mass_pair_kernel(const __grid_constant__ CUtensorMap tq, const __grid_const
     // ------------------------------------------------------------ weights and their sum
     const uint32_t acc_empty0 = mapa(smem_u32(&bar->acc_empty[0]), 0);
     const uint32_t lanes = tmem + (uint32_t((warp & 3) * 32) << 16);
-    Cursor cur(prm, bar, share);
+    Cursor<kKeys> cur(prm, bar, share);
     Item it;
     int t = 0, gi = -1;
+    float old = 0.f;                             // what this thread's key has collected so far
     while (cur.next(&it)) {
       const int cols = min(NT, prm.rows_total - it.group * NT);
-      if (it.first) {
+      if (kKeys || it.first) {
         ++gi;
         if (!wwait(&bar->lse_full, gi & 1)) break;
       }
-      // this thread's key, its page and what it has collected so far
-      const int n = it.tile * kTileKeys + (int)c * 128 + (warp & 3) * 32 + lane;
+      const int n = it.tile * kTileKeys + (int)c * 128 + (warp & 3) * 32 + lane;   // this thread's key
       float* m = a.mass + (size_t)it.b * a.mass_stride + n;
       bool live = n < it.len;
-      float old = 0.f;
       if (live) {
         const int id = a.page_table[(size_t)it.b * a.max_pages + (n >> 6)];
         live = id >= 0 && id < a.num_pages;
-        if (it.group > 0) old = *m;              // the earlier groups' sum (decay is in it)
-        else if (a.decay != 0.f && n < (a.mass_lens != nullptr ? a.mass_lens[it.b] : it.len - a.nq)) old = a.decay * *m;
+      }
+      if (it.group == 0) {
+        const int old_len = a.mass_lens != nullptr ? a.mass_lens[it.b] : it.len - a.nq;
+        old = live && a.decay != 0.f && n < old_len ? a.decay * *m : 0.f;
+      } else if (!kKeys && live) {
+        old = *m;                                // the earlier groups' sum (decay is in it)
       }
       if (!wwait(&bar->acc_full[t & 1], (t >> 1) & 1)) break;
       tc_fence_after();
@@ -387,9 +417,10 @@ attn_mass_pair_kernel(const __grid_constant__ CUtensorMap tq, const __grid_const
       __syncwarp();
       if (lane == 0) {
         mbar_arrive_cluster(acc_empty0 + 8 * (t & 1));
-        if (it.last) mbar_arrive(&bar->lse_empty);
+        if (kKeys || it.last) mbar_arrive(&bar->lse_empty);
       }
-      if (live) *m = old + ((sum[0] + sum[1]) + (sum[2] + sum[3]));
+      old += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+      if (live && (!kKeys || it.last)) *m = old;
       ++t;
     }
   }
@@ -410,16 +441,16 @@ attn_mass_pair_kernel(const __grid_constant__ CUtensorMap tq, const __grid_const
   }
 }
 
-template <int NT>
+template <int NT, bool kKeys>
 cudaError_t launch(const CUtensorMap& tq, const CUtensorMap& tp, const PairMassParams& prm, int workers,
                    cudaStream_t stream) {
-  cudaError_t e = cudaFuncSetAttribute(attn_mass_pair_kernel<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       Layout<NT>::kBytes);
+  cudaError_t e = cudaFuncSetAttribute(attn_mass_pair_kernel<NT, kKeys>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       Layout<NT, kKeys>::kBytes);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2 * workers, 1, 1);
   cfg.blockDim = dim3(kThreads, 1, 1);
-  cfg.dynamicSmemBytes = Layout<NT>::kBytes;
+  cfg.dynamicSmemBytes = Layout<NT, kKeys>::kBytes;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -429,7 +460,7 @@ cudaError_t launch(const CUtensorMap& tq, const CUtensorMap& tp, const PairMassP
   attr[1] = pdl_attribute();
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  e = cudaLaunchKernelEx(&cfg, attn_mass_pair_kernel<NT>, tq, tp, prm);
+  e = cudaLaunchKernelEx(&cfg, attn_mass_pair_kernel<NT, kKeys>, tq, tp, prm);
   if (e != cudaSuccess) return e;
   return cudaGetLastError();
 }
@@ -451,7 +482,10 @@ cudaError_t launch_attn_mass_pair(const MassArgs& a, int sms, long long spin_lim
   // one pair per two SMs, but no more pairs than the batch can have tiles
   const int64_t tiles = (int64_t)a.batch * ((a.max_pages + 3) / 4);
   const int workers = (int)(tiles < sms / 2 ? tiles : sms / 2);
-  return nt == 256 ? launch<256>(tq, tp, prm, workers, stream) : launch<128>(tq, tp, prm, workers, stream);
+  if (nt == 128) return launch<128, false>(tq, tp, prm, workers, stream);
+  // 16 groups over 2 x 32768 keys: 207 us with the tile resident, 232 with the group
+  return prm.groups > kSubTiles ? launch<256, true>(tq, tp, prm, workers, stream)
+                                : launch<256, false>(tq, tp, prm, workers, stream);
 }
 
 }  // namespace mla
