@@ -361,28 +361,40 @@ attn_mass_pair_kernel(const __grid_constant__ CUtensorMap tq, const __grid_const
     // ------------------------------------------------------------ weights and their sum
     const uint32_t acc_empty0 = mapa(smem_u32(&bar->acc_empty[0]), 0);
     const uint32_t lanes = tmem + (uint32_t((warp & 3) * 32) << 16);
+    const int row = (int)c * 128 + (warp & 3) * 32 + lane;   // this thread's key within a tile
+    // The key's page id and its mass so far are fetched an item ahead: their latency would
+    // otherwise add to each tile's sum.
     Cursor<kKeys> cur(prm, bar, share);
-    Item it;
+    Item next;
+    int next_id = -1;
+    float next_mass = 0.f;
+    auto fetch = [&]() -> bool {
+      if (!cur.next(&next)) return false;
+      const int n = next.tile * kTileKeys + row;
+      if (n < next.len) {
+        next_id = __ldg(a.page_table + (size_t)next.b * a.max_pages + (n >> 6));
+        if (next.group == 0 ? a.decay != 0.f : !kKeys) next_mass = a.mass[(size_t)next.b * a.mass_stride + n];
+      }
+      return true;
+    };
     int t = 0, gi = -1;
-    float old = 0.f;                             // what this thread's key has collected so far
-    while (cur.next(&it)) {
+    float sum_so_far = 0.f;                      // what the key has collected
+    bool more = fetch();
+    while (more) {
+      const Item it = next;
+      const int n = it.tile * kTileKeys + row;
+      const bool live = n < it.len && next_id >= 0 && next_id < a.num_pages;
+      if (it.group == 0) {
+        const int old_len = a.mass_lens != nullptr ? a.mass_lens[it.b] : it.len - a.nq;
+        sum_so_far = a.decay != 0.f && n < old_len ? a.decay * next_mass : 0.f;
+      } else if (!kKeys && !(it.first && it.last)) {
+        sum_so_far = next_mass;                  // the earlier groups' sum; of a lone tile, still here
+      }
+      more = fetch();
       const int cols = min(NT, prm.rows_total - it.group * NT);
       if (kKeys || it.first) {
         ++gi;
         if (!wwait(&bar->lse_full, gi & 1)) break;
-      }
-      const int n = it.tile * kTileKeys + (int)c * 128 + (warp & 3) * 32 + lane;   // this thread's key
-      float* m = a.mass + (size_t)it.b * a.mass_stride + n;
-      bool live = n < it.len;
-      if (live) {
-        const int id = a.page_table[(size_t)it.b * a.max_pages + (n >> 6)];
-        live = id >= 0 && id < a.num_pages;
-      }
-      if (it.group == 0) {
-        const int old_len = a.mass_lens != nullptr ? a.mass_lens[it.b] : it.len - a.nq;
-        old = live && a.decay != 0.f && n < old_len ? a.decay * *m : 0.f;
-      } else if (!kKeys && live) {
-        old = *m;                                // the earlier groups' sum (decay is in it)
       }
       if (!wwait(&bar->acc_full[t & 1], (t >> 1) & 1)) break;
       tc_fence_after();
@@ -419,8 +431,8 @@ attn_mass_pair_kernel(const __grid_constant__ CUtensorMap tq, const __grid_const
         mbar_arrive_cluster(acc_empty0 + 8 * (t & 1));
         if (kKeys || it.last) mbar_arrive(&bar->lse_empty);
       }
-      old += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-      if (live && (!kKeys || it.last)) *m = old;
+      sum_so_far += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+      if (live && (!kKeys || it.last)) a.mass[(size_t)it.b * a.mass_stride + n] = sum_so_far;
       ++t;
     }
   }
