@@ -1,20 +1,21 @@
 // Attention mass of the cached tokens on CTA pairs with 2-SM tensor-core
 // instructions (tcgen05 .cta_group::2, TMEM, TMA).
 //
-// Shape: d_c = 512, d_rope = 64 (576-wide cache rows), 64-token pages.  The product is
+// Shape: cache rows up to 576 wide (in blocks of 64 columns, the last one filled up with
+// zeros by the loads), pages of 8 to 256 tokens, a power of two.  The product is
 // transposed against the decode kernel's: the keys are its rows and the query
-// rows its columns, S[256 x NT] = K[256 x 576] . Q[NT x 576]^T, so a key's scores lie in
+// rows its columns, S[256 x NT] = K[256 x R] . Q[NT x R]^T, so a key's scores lie in
 // one TMEM lane and one thread adds up its weights: no reduction across threads,
 // no running maximum (the lse is final) and a fixed order of the sum.
 //
-//   tile    256 keys of a sequence (4 pages), 128 per CTA of the pair
+//   tile    256 keys of a sequence, 128 per CTA of the pair
 //   group   NT query rows (128 or 256), half of them in each CTA's shared memory
-// One of the two stays in shared memory (9 blocks of 64 columns) while the other goes by
+// One of the two stays in shared memory while the other goes by
 // TMA through a ring of blocks, each done with after its four MMAs; a resident block is
 // reloaded as soon as its last MMAs are through.
-//   one group   (nq * H <= 256: decode) the group stays, the keys stream: HBM binds, 295 KB
-//               per tile and pair, 6700 cycles at the pair's share of the bandwidth, against
-//               4600 of the tensor pipe at NT = 256
+//   one group   (nq * H <= 256: decode) the group stays, the keys stream: HBM binds, at R =
+//               576 with 295 KB per tile and pair, 6700 cycles at the pair's share of the
+//               bandwidth, against 4600 of the tensor pipe at NT = 256
 //   few groups  the same, the worker taking kSubTiles tiles at a time through all groups,
 //               so that the groups after the first find the keys in L2
 //   many groups the tile stays and the groups stream.  Both forms are bound by what an SM
@@ -42,7 +43,9 @@ using namespace sm100;
 
 constexpr int kThreads = 256;
 constexpr int kTileKeys = 256;
-constexpr int kBlocks = 9;                       // 64-column blocks of a 576-wide row
+constexpr int kMaxBlocks = 9;                    // 64-column blocks of a 576-wide row
+constexpr int kMaxStages = 12;                   // of the ring
+constexpr int kMaxSmem = 232448;
 constexpr int kKeyBytes = 128 * 128;             // [128 keys x 64 columns] bf16, 128-byte swizzle
 constexpr int kSubTiles = 4;                     // tiles per pass over the groups: 74 pairs hold 87 MB of keys in L2
 constexpr long long kDrainCycles = 1ll << 24;
@@ -53,21 +56,21 @@ struct Layout {
   static constexpr int kQueryBytes = NT / 2 * 128;                   // one block of this CTA's half of the group
   static constexpr int kResBytes = kKeys ? kKeyBytes : kQueryBytes;  // a block of the resident operand
   static constexpr int kRingBytes = kKeys ? kQueryBytes : kKeyBytes; // ... of the streaming one
-  static constexpr int kStages = NT == 256 ? 5 : 9;
-  static constexpr int kOffRing = kBlocks * kResBytes;
-  static constexpr int kOffLse = kOffRing + kStages * kRingBytes;    // fp32 [NT], log2 units
-  static constexpr int kOffBar = kOffLse + NT * 4;
-  static constexpr int kBytes = kOffBar + 512 + 1024;                // + 1 KB alignment slack
+  // lse (fp32 [NT], log2 units), barriers, the resident blocks, the ring; 1 KB alignment slack
+  static constexpr int kOffBar = NT * 4;
+  static constexpr int kOffRes = 2048;
+  static int stages(int blocks) {
+    const int n = (kMaxSmem - 1024 - kOffRes - blocks * kResBytes) / kRingBytes;
+    return n < kMaxStages ? n : kMaxStages;
+  }
+  static int bytes(int blocks) { return 1024 + kOffRes + blocks * kResBytes + stages(blocks) * kRingBytes; }
 };
-static_assert(Layout<256, false>::kBytes <= 232448 && Layout<128, false>::kBytes <= 232448 &&
-                  Layout<256, true>::kBytes <= 232448,
-              "shared memory budget");
 
 struct Bars {
-  uint64_t ring_full[9]; // CTA 0: both CTAs' blocks landed in the stage (2 arrivals + bytes)
-  uint64_t ring_empty[9];// both: the MMAs are done with the stage
-  uint64_t res_full[9];  // CTA 0: both CTAs' blocks of the resident operand landed
-  uint64_t res_empty[9]; // both: the MMAs are done with that block
+  uint64_t ring_full[kMaxStages];   // CTA 0: both CTAs' blocks landed in the stage (2 arrivals + bytes)
+  uint64_t ring_empty[kMaxStages];  // both: the MMAs are done with the stage
+  uint64_t res_full[kMaxBlocks];    // CTA 0: both CTAs' blocks of the resident operand landed
+  uint64_t res_empty[kMaxBlocks];   // both: the MMAs are done with that block
   uint64_t acc_full[2];  // both: a tile's scores are in TMEM
   uint64_t acc_empty[2]; // CTA 0: the 8 summing warps of the pair have read them
   uint64_t lse_full;     // local: a group's lse is in shared memory
@@ -77,12 +80,15 @@ struct Bars {
   int abort;
   int b0, tile0;         // where this worker starts
 };
-static_assert(sizeof(Bars) <= 512, "barrier area");
+static_assert(Layout<256, false>::kOffBar + sizeof(Bars) <= Layout<256, false>::kOffRes, "barrier area");
 
 struct PairMassParams {
   MassArgs m;
   int rows_total;        // nq * H
   int groups;
+  int blocks, stages;    // 64-column blocks of a row, stages of the ring
+  int page_shift;        // log2(page_size)
+  int box_rows;          // keys per TMA box: a page, or half of a 256-token one
   float scale_log2;
   long long spin_limit;
 };
@@ -90,7 +96,7 @@ struct PairMassParams {
 // A sequence's tiles; 0 when its length is out of range.
 __device__ __forceinline__ int seq_tiles(const MassArgs& a, int b, int* len) {
   *len = a.seq_lens[b];
-  return *len < a.nq || *len > a.max_pages * 64 ? 0 : (*len + kTileKeys - 1) / kTileKeys;
+  return *len < a.nq || *len > a.max_pages * a.page_size ? 0 : (*len + kTileKeys - 1) / kTileKeys;
 }
 
 // One accumulator's worth of work; every role walks the same ones in the same order.
@@ -153,7 +159,9 @@ attn_mass_pair_kernel(const __grid_constant__ CUtensorMap tq, const __grid_const
   extern __shared__ unsigned char smem_raw[];
   unsigned char* sm =
       reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  float* lse2 = reinterpret_cast<float*>(sm + L::kOffLse);
+  float* lse2 = reinterpret_cast<float*>(sm);
+  unsigned char* res_s = sm + L::kOffRes;
+  unsigned char* ring_s = res_s + prm.blocks * L::kResBytes;
   Bars* bar = reinterpret_cast<Bars*>(sm + L::kOffBar);
   volatile int* abort_flag = &bar->abort;
 
@@ -163,11 +171,14 @@ attn_mass_pair_kernel(const __grid_constant__ CUtensorMap tq, const __grid_const
   const int w = blockIdx.x >> 1, workers = gridDim.x >> 1;
   const long long lim = prm.spin_limit;
   int32_t* status = a.dev_status;
+  const int blocks = prm.blocks, stages = prm.stages;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < 9; ++s) {
+    for (int s = 0; s < kMaxStages; ++s) {
       mbar_init(&bar->ring_full[s], 2);
       mbar_init(&bar->ring_empty[s], 1);
+    }
+    for (int s = 0; s < kMaxBlocks; ++s) {
       mbar_init(&bar->res_full[s], 2);
       mbar_init(&bar->res_empty[s], 1);
     }
@@ -231,86 +242,83 @@ attn_mass_pair_kernel(const __grid_constant__ CUtensorMap tq, const __grid_const
     // ------------------------------------------------------------ queries and keys (TMA)
     const uint32_t ring_full0 = mapa(smem_u32(&bar->ring_full[0]), 0);
     const uint32_t res_full0 = mapa(smem_u32(&bar->res_full[0]), 0);
-    const int oob_row = a.num_pages * 64;        // a box starting here lies outside the pool: zero fill
+    const int oob_row = a.num_pages << prm.page_shift;   // a box starting here lies outside the pool: zero fill
     const uint64_t once = l2_policy_evict_first();
-    // the ids of this CTA's two pages of a tile are fetched while the tile before is loaded
+    // Lane j looks after the j-th box of this CTA's keys.  The page ids of a tile are
+    // fetched while the tile before is loaded.
+    const int n_boxes = 128 / prm.box_rows, box_bytes = prm.box_rows * 128;
+    const bool has_box = lane < n_boxes;
+    const int box_key = (int)c * 128 + lane * prm.box_rows;      // its first key within a tile
     Cursor<kKeys> cur(prm, bar, share);
     Item next;
-    int next_id[2] = {0, 0};
+    int next_id = 0;
     auto fetch = [&]() -> bool {
       if (!cur.next(&next)) return false;
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int pg = next.tile * 4 + (int)c * 2 + j;
-        if (pg * 64 < next.len) next_id[j] = __ldg(a.page_table + (size_t)next.b * a.max_pages + pg);
-      }
+      const int n = next.tile * kTileKeys + box_key;
+      if (has_box && n < next.len) next_id = __ldg(a.page_table + (size_t)next.b * a.max_pages + (n >> prm.page_shift));
       return true;
     };
-    int k = 0, ri = -1;                          // stages used, resident operands begun
+    int s = 0, ri = -1;                          // the ring's stage, resident operands begun
+    uint32_t lap = 0;                            // times round the ring
     bool ok = true, more = fetch();
     while (ok && more) {
       const Item it = next;
       if (it.first) ++ri;
-      int y[2];
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const bool in_seq = (it.tile * 4 + (int)c * 2 + j) * 64 < it.len;
-        const bool in_pool = next_id[j] >= 0 && next_id[j] < a.num_pages;
-        y[j] = in_seq && in_pool ? next_id[j] * 64 : oob_row;
-        if (in_seq && !in_pool && lane == 0) record_status(status, MLA_ERR_RANGE);
+      const int n = it.tile * kTileKeys + box_key;
+      int y = oob_row;
+      if (has_box && n < it.len) {
+        if (next_id >= 0 && next_id < a.num_pages)
+          y = (next_id << prm.page_shift) + (n & (a.page_size - 1));
+        else
+          record_status(status, MLA_ERR_RANGE);
       }
       more = fetch();
       const int qrow = it.b * prm.rows_total + it.group * NT + (int)c * (NT / 2);
       auto load_keys = [&](unsigned char* dst, int blk, uint32_t full) {
-        mbar_arrive_expect_tx_cluster(full, kKeyBytes);
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          if (prm.groups == 1)
-            tma_load_2d_pair_hint(dst + j * (kKeyBytes / 2), &tp, 64 * blk, y[j], full, once);
-          else
-            tma_load_2d_pair(dst + j * (kKeyBytes / 2), &tp, 64 * blk, y[j], full);
-        }
+        if (lane == 0) mbar_arrive_expect_tx_cluster(full, kKeyBytes);
+        __syncwarp();
+        if (!has_box) return;
+        if (prm.groups == 1) tma_load_2d_pair_hint(dst + lane * box_bytes, &tp, 64 * blk, y, full, once);
+        else tma_load_2d_pair(dst + lane * box_bytes, &tp, 64 * blk, y, full);
       };
       auto load_query = [&](unsigned char* dst, int blk, uint32_t full) {
+        if (lane != 0) return;
         mbar_arrive_expect_tx_cluster(full, L::kQueryBytes);
         tma_load_2d_pair(dst, &tq, 64 * blk, qrow, full);
       };
-      for (int blk = 0; blk < kBlocks; ++blk, ++k) {
+      for (int blk = 0; blk < blocks; ++blk) {
         if (it.first) {
           if (ri > 0 && !(ok = wwait(&bar->res_empty[blk], (ri - 1) & 1))) break;
-          unsigned char* dst = sm + blk * L::kResBytes;
-          if (lane == 0) {
-            if (kKeys) load_keys(dst, blk, res_full0 + 8 * blk);
-            else load_query(dst, blk, res_full0 + 8 * blk);
-          }
+          unsigned char* dst = res_s + blk * L::kResBytes;
+          if (kKeys) load_keys(dst, blk, res_full0 + 8 * blk);
+          else load_query(dst, blk, res_full0 + 8 * blk);
+          __syncwarp();
         }
-        const int s = k % L::kStages;
-        if (k >= L::kStages && !(ok = wwait(&bar->ring_empty[s], (k / L::kStages - 1) & 1))) break;
-        unsigned char* dst = sm + L::kOffRing + s * L::kRingBytes;
-        if (lane == 0) {
-          if (kKeys) load_query(dst, blk, ring_full0 + 8 * s);
-          else load_keys(dst, blk, ring_full0 + 8 * s);
-        }
+        if (lap > 0 && !(ok = wwait(&bar->ring_empty[s], (lap - 1) & 1))) break;
+        unsigned char* dst = ring_s + s * L::kRingBytes;
+        if (kKeys) load_query(dst, blk, ring_full0 + 8 * s);
+        else load_keys(dst, blk, ring_full0 + 8 * s);
         __syncwarp();
+        if (++s == stages) { s = 0; ++lap; }
       }
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer (CTA 0)
     if (c == 0) {
       const uint32_t idesc = idesc_bf16_f32(256, NT, 0, 0);
-      const uint32_t res = smem_u32(sm), ring = smem_u32(sm + L::kOffRing);
+      const uint32_t res = smem_u32(res_s), ring = smem_u32(ring_s);
       Cursor<kKeys> cur(prm, bar, share);
       Item it;
-      int k = 0, ri = -1, t = 0;
+      int s = 0, ri = -1, t = 0;
+      uint32_t lap = 0;
       bool ok = true;
       while (ok && cur.next(&it)) {
         if (it.first) ++ri;
         if (t >= 2 && !wwait(&bar->acc_empty[t & 1], ((t >> 1) - 1) & 1)) break;
         const uint32_t d = tmem + (t & 1) * NT;
-        for (int blk = 0; blk < kBlocks; ++blk, ++k) {
-          const int s = k % L::kStages;
+        for (int blk = 0; blk < blocks; ++blk) {
           if (it.first && !(ok = wwait(&bar->res_full[blk], ri & 1))) break;
-          if (!(ok = wwait(&bar->ring_full[s], (k / L::kStages) & 1))) break;
+          if (!(ok = wwait(&bar->ring_full[s], lap & 1))) break;
           tc_fence_after();
           if (elect_one()) {
             const uint32_t res_blk = res + blk * L::kResBytes, ring_blk = ring + s * L::kRingBytes;
@@ -322,9 +330,10 @@ attn_mass_pair_kernel(const __grid_constant__ CUtensorMap tq, const __grid_const
             }
             mma_commit_pair(&bar->ring_empty[s]);
             if (it.last) mma_commit_pair(&bar->res_empty[blk]);
-            if (blk == kBlocks - 1) mma_commit_pair(&bar->acc_full[t & 1]);
+            if (blk == blocks - 1) mma_commit_pair(&bar->acc_full[t & 1]);
           }
           __syncwarp();
+          if (++s == stages) { s = 0; ++lap; }
         }
         ++t;
       }
@@ -372,7 +381,7 @@ attn_mass_pair_kernel(const __grid_constant__ CUtensorMap tq, const __grid_const
       if (!cur.next(&next)) return false;
       const int n = next.tile * kTileKeys + row;
       if (n < next.len) {
-        next_id = __ldg(a.page_table + (size_t)next.b * a.max_pages + (n >> 6));
+        next_id = __ldg(a.page_table + (size_t)next.b * a.max_pages + (n >> prm.page_shift));
         if (next.group == 0 ? a.decay != 0.f : !kKeys) next_mass = a.mass[(size_t)next.b * a.mass_stride + n];
       }
       return true;
@@ -454,15 +463,16 @@ attn_mass_pair_kernel(const __grid_constant__ CUtensorMap tq, const __grid_const
 }
 
 template <int NT, bool kKeys>
-cudaError_t launch(const CUtensorMap& tq, const CUtensorMap& tp, const PairMassParams& prm, int workers,
+cudaError_t launch(const CUtensorMap& tq, const CUtensorMap& tp, PairMassParams prm, int workers,
                    cudaStream_t stream) {
-  cudaError_t e = cudaFuncSetAttribute(attn_mass_pair_kernel<NT, kKeys>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       Layout<NT, kKeys>::kBytes);
+  prm.stages = Layout<NT, kKeys>::stages(prm.blocks);
+  const int smem = Layout<NT, kKeys>::bytes(prm.blocks);
+  cudaError_t e = cudaFuncSetAttribute(attn_mass_pair_kernel<NT, kKeys>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2 * workers, 1, 1);
   cfg.blockDim = dim3(kThreads, 1, 1);
-  cfg.dynamicSmemBytes = Layout<NT, kKeys>::kBytes;
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -479,6 +489,10 @@ cudaError_t launch(const CUtensorMap& tq, const CUtensorMap& tp, const PairMassP
 
 }  // namespace
 
+bool attn_mass_pair_supported(int row, int page_size) {
+  return row <= 64 * kMaxBlocks && page_size >= 8 && (page_size & (page_size - 1)) == 0;
+}
+
 cudaError_t launch_attn_mass_pair(const MassArgs& a, int sms, long long spin_limit, cudaStream_t stream) {
   PairMassParams prm;
   prm.m = a;
@@ -487,12 +501,17 @@ cudaError_t launch_attn_mass_pair(const MassArgs& a, int sms, long long spin_lim
   prm.groups = (prm.rows_total + nt - 1) / nt;
   prm.scale_log2 = a.scale * 1.4426950408889634f;
   prm.spin_limit = spin_limit;
+  const int row = a.d_c + a.d_rope;
+  prm.blocks = (row + 63) / 64;
+  prm.page_shift = 0;
+  while ((1 << prm.page_shift) < a.page_size) ++prm.page_shift;
+  prm.box_rows = a.page_size < 128 ? a.page_size : 128;
   CUtensorMap tq, tp;
-  if (!encode_rows576(&tq, a.q_lat, (uint64_t)a.batch * prm.rows_total, 64, nt / 2, CU_TENSOR_MAP_SWIZZLE_128B) ||
-      !encode_rows576(&tp, a.pool, (uint64_t)a.num_pages * 64, 64, 64, CU_TENSOR_MAP_SWIZZLE_128B))
+  if (!encode_rows(&tq, a.q_lat, (uint64_t)a.batch * prm.rows_total, row, nt / 2) ||
+      !encode_rows(&tp, a.pool, (uint64_t)a.num_pages * a.page_size, row, prm.box_rows))
     return cudaErrorInvalidValue;
   // one pair per two SMs, but no more pairs than the batch can have tiles
-  const int64_t tiles = (int64_t)a.batch * ((a.max_pages + 3) / 4);
+  const int64_t tiles = a.batch * (((int64_t)a.max_pages * a.page_size + kTileKeys - 1) / kTileKeys);
   const int workers = (int)(tiles < sms / 2 ? tiles : sms / 2);
   if (nt == 128) return launch<128, false>(tq, tp, prm, workers, stream);
   // 16 groups over 2 x 32768 keys: 207 us with the tile resident, 232 with the group

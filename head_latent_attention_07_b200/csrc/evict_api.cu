@@ -81,7 +81,7 @@ int mla_attn_mass(const mla_dims* dims, const mla_bf16* q_lat, const mla_bf16* p
   a.page_size = dims->page_size; a.max_pages = max_pages; a.num_pages = num_pages;
   a.scale = dims->softmax_scale > 0.f ? dims->softmax_scale : 1.0f / sqrtf((float)(dims->qk_nope + dims->d_rope));
   a.decay = decay;
-  if (!mla::decode_pair_supported(a.d_c, a.d_rope, a.page_size))
+  if (!mla::attn_mass_pair_supported(a.d_c + a.d_rope, a.page_size))
     return cuda_status(mla::launch_attn_mass(a, (cudaStream_t)stream));
   int sms = 0;
   if ((st = device_sms(&sms)) != MLA_OK) return st;

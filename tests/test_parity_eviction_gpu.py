@@ -111,6 +111,9 @@ def test_mass_tensor_core_shape(nq, heads, lens):
     (128, 32, 64, 64, 2, 16, [2, 200, 65]), (192, 24, 16, 64, 1, 40, [16, 17, 333]), (8, 8, 1, 16, 1, 1, [1, 5, 40]),
     (256, 64, 64, 128, 3, 65, [3, 100]), (512, 64, 32, 128, 1, 128, [31, 33, 300]), (24, 16, 7, 32, 4, 5, [4, 50, 51]),
     (512, 256, 128, 128, 1, 9, [1, 129]), (504, 64, 64, 128, 17, 8, [17, 90]),
+    (64, 16, 8, 32, 1, 32, [1, 7, 8, 9, 130, 300]), (128, 32, 256, 64, 2, 128, [2, 255, 256, 257, 900]),
+    (256, 64, 128, 128, 8, 128, [127, 129, 700]), (192, 24, 64, 64, 5, 128, [640, 77]), (8, 8, 16, 16, 1, 128, [500]),
+    (64, 16, 48, 32, 2, 16, [2, 100, 200]),
 ])
 def test_mass_other_shapes(d_c, d_rope, page, nope, nq, heads, lens):
     check_mass(Cache(lens, nq, heads, d_c, d_rope, page, nope, seed=d_c + nq).make_lse())
