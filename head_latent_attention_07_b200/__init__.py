@@ -374,36 +374,48 @@ def mla_query_proj(dims: MlaDims, h, w_dq, w_uq, c_q, q, stream=None) -> None:
 
 
 def _pointers(*specs):
-    """Data pointers of (tensor, dtype, shape, name) after the checks of all: type and shape
-    first, then that every tensor is dense and on the current device, where the call
-    launches.  An optional tensor that is None gives None."""
+    """Data pointers of (tensor, dtype, shape, name), None for an optional tensor that is
+    None.  Every tensor must be dense and on the current device, where the call launches."""
+    out = []
+    device = None
+    try:
+        for t, dtype, shape, _ in specs:
+            if t is None:
+                out.append(None)
+                continue
+            index = t.get_device()
+            if device is None and index >= 0:
+                device = _torch().cuda.current_device()
+            if t.dtype is not dtype or index != device or not t.is_contiguous() or (shape is not None and t.shape != shape):
+                break
+            out.append(t.data_ptr())
+        else:
+            return out
+    except AttributeError:      # not a tensor
+        pass
+    _refuse(specs)
+
+
+def _refuse(specs):
+    """Raises for the first tensor that _pointers refuses: types and shapes first."""
     torch = _torch()
+    specs = [s for s in specs if s[0] is not None]
     for t, dtype, shape, name in specs:
-        if t is None:
-            continue
         if not isinstance(t, torch.Tensor):
             raise TypeError(f"{name} must be a torch.Tensor")
         if t.dtype != dtype:
             raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
         if shape is not None and t.shape != shape:
             raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    device = None
-    out = []
-    for t, dtype, shape, name in specs:
-        if t is None:
-            out.append(None)
-            continue
-        index = t.get_device()
-        if index < 0:
+    for t, _, _, name in specs:
+        if not t.is_cuda:
             raise ValueError(f"{name} must be a CUDA tensor")
         if not t.is_contiguous():
             raise ValueError(f"{name} must be contiguous")
-        if device is None:
-            device = torch.cuda.current_device()
-        if index != device:
-            raise ValueError(f"{name} is on cuda:{index}, the current device is cuda:{device}")
-        out.append(t.data_ptr())
-    return out
+    for t, _, _, name in specs:
+        if t.get_device() != torch.cuda.current_device():
+            raise ValueError(f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+    raise ValueError("tensors refused")
 
 
 def _matrix(t, rows, name):

@@ -254,7 +254,7 @@ cudaError_t launch_cache_compact(const CompactArgs& a, int sms, cudaStream_t str
   const int smem = (int)sizeof(CompactSmem);
   cudaError_t e = cudaFuncSetAttribute(cache_compact_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  e = cudaFuncSetAttribute(cache_compact_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (geo.cluster > 8) e = cudaFuncSetAttribute(cache_compact_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
