@@ -13,7 +13,7 @@
 // the rows into slices of columns, which know nothing of each other; with few sequences
 // also from a cluster of CTAs per slice, each taking every cluster-size-th tile.  The RoPE
 // part is cut into narrower slices than the latent: turning it costs more than moving
-// it.  The mass moves with the first slice.
+// it.  The mass is one more slice.
 //
 // A CTA's threads go round by round, a tile each: start the copies of a later tile
 // (cp.async into a ring), wait until this round's tile has landed in all CTAs of the
@@ -34,14 +34,14 @@ using namespace sm100;
 
 constexpr int kThreads = 512;
 constexpr int kPieces = 2;                       // 16-byte pieces of a tile per thread
-constexpr int kTilePieces = kThreads * kPieces;  // 16 KB
+constexpr int kTileBytes = kThreads * kPieces * 16;   // 16 KB
 constexpr int kAhead = 4;                        // rounds from the start of a tile's copies to its write
 constexpr int kStages = kAhead + 1;              // ring of tiles: 80 KB, two CTAs per SM
 constexpr int kBatch = 4;                        // tiles whose rows are looked up together
 constexpr int kMaxTileRows = kThreads / kBatch;
 constexpr int kMaxCluster = 16;
 constexpr int kMinVecs = 8, kMaxVecs = 64;       // 16-byte pieces of a latent slice
-static_assert(kAhead == kBatch, "a batch is looked up a batch before its first load");
+static_assert(kAhead == kBatch, "a tile's copies start a batch before its write");
 
 __device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
@@ -52,6 +52,7 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
 // (x, y) of a RoPE pair turned by delta positions; turn = 2^64 times the pair's
 // rotation per position as a fraction of a full turn.  delta * turn modulo 2^64 is the
 // whole rotation modulo one turn, exactly, so far moves keep their phase.  Its upper 23
@@ -95,7 +96,7 @@ cache_compact_kernel(const __grid_constant__ CompactArgs a, const __grid_constan
   const int rank = (int)cluster_ctarank();
   const int slice = blockIdx.x / cluster;
   const int b = blockIdx.y;
-  const bool with_mass = a.mass != nullptr && slice == 0;
+  const bool moves_mass = slice == geo.plain_slices + geo.turn_slices;   // the mass has a slice of its own
 
   for (int i = tid; i < a.d_rope / 2; i += kThreads) sm->turn[i] = a.turn[i];
   grid_dependency_wait();
@@ -109,22 +110,25 @@ cache_compact_kernel(const __grid_constant__ CompactArgs a, const __grid_constan
   // this slice: pieces [vec0, vec0 + n_vecs) of a row
   const int vecs = (a.d_c + a.d_rope) / 8, latent = a.d_c / 8;
   const int plain = a.rerotate ? latent : vecs;
-  const bool turns = slice >= geo.plain_slices;
+  const bool turns = slice >= geo.plain_slices && !moves_mass;
   const int vec0 = turns ? plain + (slice - geo.plain_slices) * geo.turn_vecs : slice * geo.plain_vecs;
-  const int n_vecs = turns ? min(geo.turn_vecs, vecs - vec0) : min(geo.plain_vecs, plain - vec0);
-  const int rows = min(kMaxTileRows, kThreads * kPieces / n_vecs);       // of a tile
-  const int64_t row_bytes = (int64_t)vecs * 16;
-  float* mass = with_mass ? a.mass + (size_t)b * a.mass_stride : nullptr;
+  const int n_vecs = moves_mass ? 0 : turns ? min(geo.turn_vecs, vecs - vec0) : min(geo.plain_vecs, plain - vec0);
+  const int rows = moves_mass ? kMaxTileRows : min(kMaxTileRows, kThreads * kPieces / n_vecs);   // of a tile
+  const uint32_t row_bytes = vecs * 16;
+  float* mass = a.mass + (size_t)b * a.mass_stride;
   const int rounds = (new_len + rows * cluster - 1) / (rows * cluster);
 
-  // this thread's pieces of every tile: the row within the tile and the place in the row
-  int row_of[kPieces];
+  // this thread's pieces of every tile: the row within the tile (of its slice, -1: none)
+  // and the place in the row
+  int row_of[kPieces], turn_of[kPieces];
   char* pool_at[kPieces];
 #pragma unroll
   for (int k = 0; k < kPieces; ++k) {
     const int i = tid + k * kThreads;
+    const int p = n_vecs > 0 ? i % n_vecs : 0;
     row_of[k] = i < rows * n_vecs ? i / n_vecs : -1;
-    pool_at[k] = reinterpret_cast<char*>(a.pool) + (vec0 + i % n_vecs) * 16;
+    pool_at[k] = reinterpret_cast<char*>(a.pool) + (vec0 + p) * 16;
+    turn_of[k] = (vec0 - latent + p) * 4;
   }
   const uint32_t ring0 = smem_u32(&sm->ring[0][tid]);
 
@@ -153,7 +157,7 @@ cache_compact_kernel(const __grid_constant__ CompactArgs a, const __grid_constan
     }
     n_next = index_of(batch + 1);
   };
-  auto resolve = [&](int batch) {
+  auto resolve = [&](int slot2, int slot3) {   // into these slots of the batches' rings
     uint32_t src = kNone, dst = kNone;
     if (n_now >= 0) {
       if ((uint32_t)src_page < (uint32_t)a.num_pages && (uint32_t)dst_page < (uint32_t)a.num_pages) {
@@ -163,22 +167,23 @@ cache_compact_kernel(const __grid_constant__ CompactArgs a, const __grid_constan
         record_status(a.dev_status, MLA_ERR_RANGE);
       }
     }
-    sm->src[batch & 1][tid] = src;
-    sm->dst[batch % 3][tid] = dst;
-    sm->delta[batch % 3][tid] = n_now >= 0 ? j_now - n_now : 0;
+    sm->src[slot2][tid] = src;
+    sm->dst[slot3][tid] = dst;
+    sm->delta[slot3][tid] = n_now >= 0 ? j_now - n_now : 0;
   };
-  auto load = [&](int r, int stage) {
+  // tile r into a stage.  What is read from shared memory is read first: a load does not
+  // pass the copies.
+  auto load = [&](int r, int stage, const uint32_t* src_of, const int* delta_of) {
     if (r < rounds) {
-      const uint32_t* src_of = &sm->src[(r / kBatch) & 1][r % kBatch * kMaxTileRows];
+      uint32_t src[kPieces];
 #pragma unroll
-      for (int k = 0; k < kPieces; ++k) {
-        if (row_of[k] < 0) continue;
-        const uint32_t src = src_of[row_of[k]];
-        if (src != kNone)
-          cp_async16(ring0 + stage * (kThreads * kPieces * 16) + k * (kThreads * 16), pool_at[k] + src * row_bytes);
-      }
-      if (with_mass && tid < rows) {
-        const int d = sm->delta[r / kBatch % 3][r % kBatch * kMaxTileRows + tid];
+      for (int k = 0; k < kPieces; ++k) src[k] = row_of[k] >= 0 ? src_of[row_of[k]] : kNone;
+#pragma unroll
+      for (int k = 0; k < kPieces; ++k)
+        if (src[k] != kNone)
+          cp_async16(ring0 + stage * kTileBytes + k * (kThreads * 16), pool_at[k] + (uint64_t)src[k] * row_bytes);
+      if (moves_mass && tid < rows) {
+        const int d = delta_of[tid];
         if (d != 0) cp_async4(smem_u32(&sm->mass[stage][tid]), mass + position(r, tid) - d);
       }
     }
@@ -186,48 +191,62 @@ cache_compact_kernel(const __grid_constant__ CompactArgs a, const __grid_constan
   };
 
   look_up(0);
-  resolve(0);
+  resolve(0, 0);
   look_up(1);
-  resolve(1);
+  resolve(1, 1);
   look_up(2);
   __syncthreads();
-  for (int r = 0; r < kAhead; ++r) load(r, r);
-  int stage = 0;                               // r % kStages
-  for (int r = 0; r < rounds; ++r) {
-    load(r + kAhead, stage == 0 ? kStages - 1 : stage - 1);
-    cp_async_wait<kAhead>();                   // tile r is here
-    if (cluster > 1) {
-      __syncwarp();
-      cluster_arrive_relaxed();                // orders nothing: the copies have landed
-    }
-    if (r % kBatch == kBatch - 1) {
-      resolve(r / kBatch + 2);
-      look_up(r / kBatch + 3);
-      __syncthreads();
-    } else if (cluster == 1) {
-      __syncthreads();
-    }
-    if (cluster > 1) cluster_wait();           // all reads of tiles <= r, in every CTA, are done
-    const uint32_t* dst_of = &sm->dst[r / kBatch % 3][r % kBatch * kMaxTileRows];
-    const int* delta_of = &sm->delta[r / kBatch % 3][r % kBatch * kMaxTileRows];
 #pragma unroll
-    for (int k = 0; k < kPieces; ++k) {
-      if (row_of[k] < 0) continue;
-      const uint32_t dst = dst_of[row_of[k]];
-      if (dst == kNone) continue;
-      uint4 u = sm->ring[stage][tid + k * kThreads];
-      if (turns) {
-        const uint64_t* turn = sm->turn + (vec0 - latent + (tid + k * kThreads) % n_vecs) * 4;
-        const int d = delta_of[row_of[k]];
-        u.x = turn_pair(u.x, d, turn[0]);
-        u.y = turn_pair(u.y, d, turn[1]);
-        u.z = turn_pair(u.z, d, turn[2]);
-        u.w = turn_pair(u.w, d, turn[3]);
+  for (int r = 0; r < kAhead; ++r) load(r, r, &sm->src[0][r * kMaxTileRows], &sm->delta[0][r * kMaxTileRows]);
+  int stage = 0;                               // of tile r
+  int now3 = 0;                                // the slot of the batch being written in a ring of three
+  for (int batch = 0; batch * kBatch < rounds; ++batch) {
+    const int next3 = now3 == 2 ? 0 : now3 + 1, after3 = next3 == 2 ? 0 : next3 + 1;
+#pragma unroll
+    for (int t = 0; t < kBatch; ++t) {
+      const int r = batch * kBatch + t;
+      if (r >= rounds) break;
+      load(r + kAhead, stage == 0 ? kStages - 1 : stage - 1, &sm->src[(batch + 1) & 1][t * kMaxTileRows],
+           &sm->delta[next3][t * kMaxTileRows]);
+      cp_async_wait<kAhead>();                 // tile r is here
+      if (cluster > 1) {
+        __syncwarp();
+        cluster_arrive_relaxed();              // orders nothing: the copies have landed
       }
-      *reinterpret_cast<uint4*>(pool_at[k] + dst * row_bytes) = u;
+      if (t == kBatch - 1) {
+        resolve(batch & 1, after3);
+        look_up(batch + 3);
+        __syncthreads();
+      } else if (cluster == 1) {
+        __syncthreads();
+      }
+      if (cluster > 1) cluster_wait();         // all reads of tiles <= r, in every CTA, are done
+      const uint32_t* dst_of = &sm->dst[now3][t * kMaxTileRows];
+      const int* delta_of = &sm->delta[now3][t * kMaxTileRows];
+      uint32_t dst[kPieces];
+      uint4 u[kPieces];
+#pragma unroll
+      for (int k = 0; k < kPieces; ++k) {
+        dst[k] = row_of[k] >= 0 ? dst_of[row_of[k]] : kNone;
+        u[k] = sm->ring[stage][tid + k * kThreads];
+      }
+#pragma unroll
+      for (int k = 0; k < kPieces; ++k) {
+        if (dst[k] == kNone) continue;
+        if (turns) {
+          const uint64_t* turn = sm->turn + turn_of[k];
+          const int d = delta_of[row_of[k]];
+          u[k].x = turn_pair(u[k].x, d, turn[0]);
+          u[k].y = turn_pair(u[k].y, d, turn[1]);
+          u[k].z = turn_pair(u[k].z, d, turn[2]);
+          u[k].w = turn_pair(u[k].w, d, turn[3]);
+        }
+        *reinterpret_cast<uint4*>(pool_at[k] + (uint64_t)dst[k] * row_bytes) = u[k];
+      }
+      if (moves_mass && tid < rows && delta_of[tid] != 0) mass[position(r, tid)] = sm->mass[stage][tid];
+      if (++stage == kStages) stage = 0;
     }
-    if (with_mass && tid < rows && delta_of[tid] != 0) mass[position(r, tid)] = sm->mass[stage][tid];
-    if (++stage == kStages) stage = 0;
+    now3 = next3;
   }
   cp_async_wait<0>();
 }
@@ -237,17 +256,21 @@ cache_compact_kernel(const __grid_constant__ CompactArgs a, const __grid_constan
 cudaError_t launch_cache_compact(const CompactArgs& a, int sms, cudaStream_t stream) {
   const int vecs = (a.d_c + a.d_rope) / 8, plain = a.rerotate ? a.d_c / 8 : vecs, turned = vecs - plain;
   Geometry geo;
-  // the widest slices (the longest pieces of a row) that give every SM a CTA; then clusters
-  // while two CTAs per SM hold them all
+  // The widest slices (the longest pieces of a row) that give every SM a CTA; then a
+  // cluster per slice, up to the two CTAs per SM that run at a time.  With long sequences
+  // up to three: the slices that turn, or move the mass, finish early.  16 x 32768
+  // tokens, half kept: 148 us with 13 slices each, 135 with clusters of two; 8 x 4096: 11.4
+  // us with clusters of two, 12.9 with four.
   int64_t sets = 0;
   for (geo.plain_vecs = kMaxVecs;; geo.plain_vecs /= 2) {
     geo.turn_vecs = geo.plain_vecs / 4;
     geo.plain_slices = (plain + geo.plain_vecs - 1) / geo.plain_vecs;
     geo.turn_slices = (turned + geo.turn_vecs - 1) / geo.turn_vecs;
-    sets = (int64_t)(geo.plain_slices + geo.turn_slices) * a.batch;
+    sets = (int64_t)(geo.plain_slices + geo.turn_slices + (a.mass != nullptr ? 1 : 0)) * a.batch;
     if (sets >= sms || geo.plain_vecs == kMinVecs) break;
   }
-  for (geo.cluster = 1; geo.cluster < kMaxCluster && 2 * geo.cluster * sets <= 2 * sms;) geo.cluster *= 2;
+  const int64_t ctas = (int64_t)a.max_pages * a.page_size >= 16384 ? 3 * sms : 2 * sms;
+  for (geo.cluster = 1; geo.cluster < kMaxCluster && 2 * geo.cluster * sets <= ctas;) geo.cluster *= 2;
   geo.page_shift = -1;
   if ((a.page_size & (a.page_size - 1)) == 0)
     for (geo.page_shift = 0; (1 << geo.page_shift) < a.page_size; ++geo.page_shift) {}
@@ -263,7 +286,7 @@ cudaError_t launch_cache_compact(const CompactArgs& a, int sms, cudaStream_t str
   attr[0].val.clusterDim.z = 1;
   attr[1] = pdl_attribute();
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((geo.plain_slices + geo.turn_slices) * geo.cluster, a.batch, 1);
+  cfg.gridDim = dim3((geo.plain_slices + geo.turn_slices + (a.mass != nullptr ? 1 : 0)) * geo.cluster, a.batch, 1);
   cfg.blockDim = dim3(kThreads, 1, 1);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
