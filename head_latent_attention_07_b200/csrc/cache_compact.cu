@@ -10,18 +10,20 @@
 // tiles touch rows that no write so far has reached.
 //
 // Bytes bind it: two row widths per moved row.  The parallel work comes from splitting
-// the rows into slices of columns, which know nothing of each other; with few sequences
-// also from a cluster of CTAs per slice, each taking every cluster-size-th tile.  The RoPE
-// part is cut into narrower slices than the latent: turning it costs more than moving
-// it.  The mass is one more slice.
+// the rows into slices of columns, which know nothing of each other, and from a
+// cluster of CTAs per slice, each taking every cluster-size-th tile.  Every slice has
+// its share of the latent and of the RoPE columns, so that all CTAs take the same time
+// (turning costs more than moving); the mass moves with the last slice.
 //
 // A CTA's threads go round by round, a tile each: start the copies of a later tile
 // (cp.async into a ring), wait until this round's tile has landed in all CTAs of the
 // cluster, write it.  A thread writes the 16-byte pieces that it loaded, the same of every
-// tile, so the ring needs no barrier of its own.  An index leads to two page ids and those to
-// the rows: each thread looks up one row of every kBatch tiles, and its three
-// dependent loads are a batch apart.  (One bulk copy per row, by one thread, was bound
-// by its issue, 40 ns each; roles in warps of their own, by the six hand-overs of a tile.)
+// tile, so the ring needs no barrier of its own; the latent pieces of a tile come first,
+// then those of the RoPE part, so that few warps turn and all their lanes do.  An
+// index leads to two page ids and those to the rows: each thread looks up one row of
+// every kBatch tiles, and its three dependent loads are a batch apart.  (One bulk copy per
+// row, by one thread, was bound by its issue, 40 ns each; roles in warps of their own,
+// by the six hand-overs of a tile.)
 #include "common.cuh"
 #include "evict.h"
 #include "sm100.cuh"
@@ -40,12 +42,9 @@ constexpr int kStages = kAhead + 1;              // ring of tiles: 80 KB, two CT
 constexpr int kBatch = 4;                        // tiles whose rows are looked up together
 constexpr int kMaxTileRows = kThreads / kBatch;
 constexpr int kMaxCluster = 16;
-constexpr int kMinVecs = 8, kMaxVecs = 64;       // 16-byte pieces of a latent slice
+constexpr int kMaxSlices = 8;
 static_assert(kAhead == kBatch, "a tile's copies start a batch before its write");
 
-__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
-}
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
@@ -69,8 +68,9 @@ __device__ __forceinline__ uint32_t turn_pair(uint32_t xy, int delta, uint64_t t
 
 struct Geometry {
   int cluster;                     // CTAs that share a sequence's slice
-  int plain_vecs, plain_slices;    // 16-byte pieces of a slice of the columns that are only moved, and their slices
-  int turn_vecs, turn_slices;      // the same for the columns that are turned
+  int slices;                      // of a row
+  int plain_vecs, turn_vecs;       // 16-byte pieces that a slice moves, and moves and turns, at most
+  int turn_slice0;                 // the first slice that turns
   int page_shift;                  // log2(page_size), or -1
 };
 
@@ -83,7 +83,7 @@ struct CompactSmem {
   uint32_t src[2][kThreads];
   uint32_t dst[3][kThreads];
   int delta[3][kThreads];
-  float mass[kStages][kMaxTileRows];
+  float mass[3][kThreads];
   uint64_t turn[kMaxRopePairs];
 };
 
@@ -96,7 +96,7 @@ cache_compact_kernel(const __grid_constant__ CompactArgs a, const __grid_constan
   const int rank = (int)cluster_ctarank();
   const int slice = blockIdx.x / cluster;
   const int b = blockIdx.y;
-  const bool moves_mass = slice == geo.plain_slices + geo.turn_slices;   // the mass has a slice of its own
+  const bool moves_mass = a.mass != nullptr && slice == geo.slices - 1;
 
   for (int i = tid; i < a.d_rope / 2; i += kThreads) sm->turn[i] = a.turn[i];
   grid_dependency_wait();
@@ -107,28 +107,34 @@ cache_compact_kernel(const __grid_constant__ CompactArgs a, const __grid_constan
     return;                                    // the whole cluster
   }
 
-  // this slice: pieces [vec0, vec0 + n_vecs) of a row
+  // this slice: n_plain 16-byte pieces of a row that are only moved, n_turn that are turned
   const int vecs = (a.d_c + a.d_rope) / 8, latent = a.d_c / 8;
   const int plain = a.rerotate ? latent : vecs;
-  const bool turns = slice >= geo.plain_slices && !moves_mass;
-  const int vec0 = turns ? plain + (slice - geo.plain_slices) * geo.turn_vecs : slice * geo.plain_vecs;
-  const int n_vecs = moves_mass ? 0 : turns ? min(geo.turn_vecs, vecs - vec0) : min(geo.plain_vecs, plain - vec0);
-  const int rows = moves_mass ? kMaxTileRows : min(kMaxTileRows, kThreads * kPieces / n_vecs);   // of a tile
+  const int plain0 = slice * geo.plain_vecs, turn0 = plain + (slice - geo.turn_slice0) * geo.turn_vecs;
+  const int n_plain = max(0, min(geo.plain_vecs, plain - plain0));
+  const int n_turn = slice < geo.turn_slice0 ? 0 : max(0, min(geo.turn_vecs, vecs - turn0));
+  const int rows = min(kMaxTileRows, kThreads * kPieces / max(1, n_plain + n_turn));   // of a tile
   const uint32_t row_bytes = vecs * 16;
   float* mass = a.mass + (size_t)b * a.mass_stride;
   const int rounds = (new_len + rows * cluster - 1) / (rows * cluster);
 
-  // this thread's pieces of every tile: the row within the tile (of its slice, -1: none)
-  // and the place in the row
-  int row_of[kPieces], turn_of[kPieces];
+  // this thread's pieces of every tile: the row within the tile (-1: none) and the place in
+  // the row
+  int row_of[kPieces], turn_of[kPieces];       // its first pair in the turns (-1: only moved)
   char* pool_at[kPieces];
 #pragma unroll
   for (int k = 0; k < kPieces; ++k) {
-    const int i = tid + k * kThreads;
-    const int p = n_vecs > 0 ? i % n_vecs : 0;
-    row_of[k] = i < rows * n_vecs ? i / n_vecs : -1;
-    pool_at[k] = reinterpret_cast<char*>(a.pool) + (vec0 + p) * 16;
-    turn_of[k] = (vec0 - latent + p) * 4;
+    int i = tid + k * kThreads, vec = 0;
+    row_of[k] = turn_of[k] = -1;
+    if (i < rows * n_plain) {
+      row_of[k] = i / n_plain;
+      vec = plain0 + i % n_plain;
+    } else if ((i -= rows * n_plain) < rows * n_turn) {
+      row_of[k] = i / n_turn;
+      vec = turn0 + i % n_turn;
+      turn_of[k] = (vec - latent) * 4;
+    }
+    pool_at[k] = reinterpret_cast<char*>(a.pool) + vec * 16;
   }
   const uint32_t ring0 = smem_u32(&sm->ring[0][tid]);
 
@@ -145,7 +151,8 @@ cache_compact_kernel(const __grid_constant__ CompactArgs a, const __grid_constan
   auto in_page = [&](int n) { return shift >= 0 ? n & (a.page_size - 1) : n % a.page_size; };
   int n_next = index_of(0);                    // the next batch's index, and what was found with the
   int j_now = 0, n_now = -1;                   // current one's: position, source index (-1: nothing
-  int src_page = 0, dst_page = 0;              // moves) and page ids
+  int src_page = 0, dst_page = 0;              // moves), page ids and mass
+  float mass_now = 0.f;
   auto look_up = [&](int batch) {              // the pages of `batch`, the indices of the one after it
     j_now = position(batch * kBatch + tile, row);
     n_now = n_next;
@@ -154,6 +161,7 @@ cache_compact_kernel(const __grid_constant__ CompactArgs a, const __grid_constan
     if (n_now >= 0) {
       src_page = page_of(n_now);
       dst_page = page_of(j_now);
+      if (moves_mass) mass_now = __ldcg(mass + n_now);
     }
     n_next = index_of(batch + 1);
   };
@@ -170,10 +178,11 @@ cache_compact_kernel(const __grid_constant__ CompactArgs a, const __grid_constan
     sm->src[slot2][tid] = src;
     sm->dst[slot3][tid] = dst;
     sm->delta[slot3][tid] = n_now >= 0 ? j_now - n_now : 0;
+    if (moves_mass) sm->mass[slot3][tid] = mass_now;
   };
   // tile r into a stage.  What is read from shared memory is read first: a load does not
   // pass the copies.
-  auto load = [&](int r, int stage, const uint32_t* src_of, const int* delta_of) {
+  auto load = [&](int r, int stage, const uint32_t* src_of) {
     if (r < rounds) {
       uint32_t src[kPieces];
 #pragma unroll
@@ -182,10 +191,6 @@ cache_compact_kernel(const __grid_constant__ CompactArgs a, const __grid_constan
       for (int k = 0; k < kPieces; ++k)
         if (src[k] != kNone)
           cp_async16(ring0 + stage * kTileBytes + k * (kThreads * 16), pool_at[k] + (uint64_t)src[k] * row_bytes);
-      if (moves_mass && tid < rows) {
-        const int d = delta_of[tid];
-        if (d != 0) cp_async4(smem_u32(&sm->mass[stage][tid]), mass + position(r, tid) - d);
-      }
     }
     cp_async_commit();
   };
@@ -197,7 +202,7 @@ cache_compact_kernel(const __grid_constant__ CompactArgs a, const __grid_constan
   look_up(2);
   __syncthreads();
 #pragma unroll
-  for (int r = 0; r < kAhead; ++r) load(r, r, &sm->src[0][r * kMaxTileRows], &sm->delta[0][r * kMaxTileRows]);
+  for (int r = 0; r < kAhead; ++r) load(r, r, &sm->src[0][r * kMaxTileRows]);
   int stage = 0;                               // of tile r
   int now3 = 0;                                // the slot of the batch being written in a ring of three
   for (int batch = 0; batch * kBatch < rounds; ++batch) {
@@ -206,8 +211,7 @@ cache_compact_kernel(const __grid_constant__ CompactArgs a, const __grid_constan
     for (int t = 0; t < kBatch; ++t) {
       const int r = batch * kBatch + t;
       if (r >= rounds) break;
-      load(r + kAhead, stage == 0 ? kStages - 1 : stage - 1, &sm->src[(batch + 1) & 1][t * kMaxTileRows],
-           &sm->delta[next3][t * kMaxTileRows]);
+      load(r + kAhead, stage == 0 ? kStages - 1 : stage - 1, &sm->src[(batch + 1) & 1][t * kMaxTileRows]);
       cp_async_wait<kAhead>();                 // tile r is here
       if (cluster > 1) {
         __syncwarp();
@@ -233,7 +237,7 @@ cache_compact_kernel(const __grid_constant__ CompactArgs a, const __grid_constan
 #pragma unroll
       for (int k = 0; k < kPieces; ++k) {
         if (dst[k] == kNone) continue;
-        if (turns) {
+        if (turn_of[k] >= 0) {
           const uint64_t* turn = sm->turn + turn_of[k];
           const int d = delta_of[row_of[k]];
           u[k].x = turn_pair(u[k].x, d, turn[0]);
@@ -243,7 +247,8 @@ cache_compact_kernel(const __grid_constant__ CompactArgs a, const __grid_constan
         }
         *reinterpret_cast<uint4*>(pool_at[k] + (uint64_t)dst[k] * row_bytes) = u[k];
       }
-      if (moves_mass && tid < rows && delta_of[tid] != 0) mass[position(r, tid)] = sm->mass[stage][tid];
+      if (moves_mass && tid < rows && delta_of[tid] != 0)
+        mass[position(r, tid)] = sm->mass[now3][t * kMaxTileRows + tid];
       if (++stage == kStages) stage = 0;
     }
     now3 = next3;
@@ -256,21 +261,35 @@ cache_compact_kernel(const __grid_constant__ CompactArgs a, const __grid_constan
 cudaError_t launch_cache_compact(const CompactArgs& a, int sms, cudaStream_t stream) {
   const int vecs = (a.d_c + a.d_rope) / 8, plain = a.rerotate ? a.d_c / 8 : vecs, turned = vecs - plain;
   Geometry geo;
-  // The widest slices (the longest pieces of a row) that give every SM a CTA; then a
-  // cluster per slice, up to the two CTAs per SM that run at a time.  With long sequences
-  // up to three: the slices that turn, or move the mass, finish early.  16 x 32768
-  // tokens, half kept: 148 us with 13 slices each, 135 with clusters of two; 8 x 4096: 11.4
-  // us with clusters of two, 12.9 with four.
-  int64_t sets = 0;
-  for (geo.plain_vecs = kMaxVecs;; geo.plain_vecs /= 2) {
-    geo.turn_vecs = geo.plain_vecs / 4;
-    geo.plain_slices = (plain + geo.plain_vecs - 1) / geo.plain_vecs;
-    geo.turn_slices = (turned + geo.turn_vecs - 1) / geo.turn_vecs;
-    sets = (int64_t)(geo.plain_slices + geo.turn_slices + (a.mass != nullptr ? 1 : 0)) * a.batch;
-    if (sets >= sms || geo.plain_vecs == kMinVecs) break;
+  // Slices of a row: up to 8 of at least 128 bytes, as many as leave every other SM free of
+  // them; then a cluster for each, up to one CTA per SM (two CTAs on an SM slow each other's
+  // stores down), or two with few sequences, while a CTA has two tiles.  Half kept, us:
+  //   sequences x tokens   slices x cluster
+  //   64 x 8192            1 x 2  108   2 x 1  104   4 x 1  127
+  //   32 x 16384           1 x 4  134   2 x 2  108   4 x 2  128
+  //   16 x 32768           2 x 4  134   4 x 2  110   4 x 4  133   8 x 1  147
+  //    8 x 32768           4 x 4   72   8 x 2   62   8 x 4   68
+  //    4 x 32768           4 x 4   56   8 x 4   44   8 x 8   32
+  const int64_t tiles = ((int64_t)a.max_pages * a.page_size + kMaxTileRows - 1) / kMaxTileRows;
+  geo.slices = 1;
+  while (geo.slices < kMaxSlices && geo.slices * 16 <= plain && (int64_t)4 * geo.slices * a.batch <= sms) geo.slices *= 2;
+  int64_t sets = (int64_t)geo.slices * a.batch;
+  const int64_t ctas = 4 * sets <= sms ? 2 * sms : sms;
+  for (geo.cluster = 1; geo.cluster < kMaxCluster && 2 * geo.cluster * sets <= ctas && 4 * geo.cluster <= tiles;)
+    geo.cluster *= 2;
+  geo.turn_slice0 = 0;
+  if (geo.cluster == kMaxCluster && kMaxCluster * sets < sms) {
+    // a sequence alone: SMs are left over for slices of the RoPE part of their own (131072
+    // tokens, nine tenths kept: 66 us, against 88)
+    geo.plain_vecs = 8;
+    geo.turn_vecs = 2;
+    geo.turn_slice0 = (plain + 7) / 8;
+    geo.slices = geo.turn_slice0 + (turned + 1) / 2;
+  } else {
+    auto share = [&](int n) { return ((n + geo.slices - 1) / geo.slices + 1) & ~1; };   // whole 32-byte sectors
+    geo.plain_vecs = share(plain);
+    geo.turn_vecs = share(turned);
   }
-  const int64_t ctas = (int64_t)a.max_pages * a.page_size >= 16384 ? 3 * sms : 2 * sms;
-  for (geo.cluster = 1; geo.cluster < kMaxCluster && 2 * geo.cluster * sets <= ctas;) geo.cluster *= 2;
   geo.page_shift = -1;
   if ((a.page_size & (a.page_size - 1)) == 0)
     for (geo.page_shift = 0; (1 << geo.page_shift) < a.page_size; ++geo.page_shift) {}
@@ -286,7 +305,7 @@ cudaError_t launch_cache_compact(const CompactArgs& a, int sms, cudaStream_t str
   attr[0].val.clusterDim.z = 1;
   attr[1] = pdl_attribute();
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((geo.plain_slices + geo.turn_slices + (a.mass != nullptr ? 1 : 0)) * geo.cluster, a.batch, 1);
+  cfg.gridDim = dim3(geo.slices * geo.cluster, a.batch, 1);
   cfg.blockDim = dim3(kThreads, 1, 1);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
