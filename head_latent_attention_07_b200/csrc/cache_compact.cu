@@ -263,18 +263,20 @@ cudaError_t launch_cache_compact(const CompactArgs& a, int sms, cudaStream_t str
   Geometry geo;
   // Slices of a row: up to 8 of at least 128 bytes, as many as leave every other SM free of
   // them; then a cluster for each, up to one CTA per SM (two CTAs on an SM slow each other's
-  // stores down), or two with few sequences, while a CTA has two tiles.  Half kept, us:
+  // stores down), or two with few or short sequences, where latency counts, while a CTA has
+  // two tiles.  Half kept, us:
   //   sequences x tokens   slices x cluster
   //   64 x 8192            1 x 2  108   2 x 1  104   4 x 1  127
   //   32 x 16384           1 x 4  134   2 x 2  108   4 x 2  128
   //   16 x 32768           2 x 4  134   4 x 2  110   4 x 4  133   8 x 1  147
   //    8 x 32768           4 x 4   72   8 x 2   62   8 x 4   68
   //    4 x 32768           4 x 4   56   8 x 4   44   8 x 8   32
+  //    8 x 4096            8 x 2   16   8 x 4   11
   const int64_t tiles = ((int64_t)a.max_pages * a.page_size + kMaxTileRows - 1) / kMaxTileRows;
   geo.slices = 1;
   while (geo.slices < kMaxSlices && geo.slices * 16 <= plain && (int64_t)4 * geo.slices * a.batch <= sms) geo.slices *= 2;
   int64_t sets = (int64_t)geo.slices * a.batch;
-  const int64_t ctas = 4 * sets <= sms ? 2 * sms : sms;
+  const int64_t ctas = 4 * sets <= sms || tiles * kMaxTileRows < 8192 ? 2 * sms : sms;
   for (geo.cluster = 1; geo.cluster < kMaxCluster && 2 * geo.cluster * sets <= ctas && 4 * geo.cluster <= tiles;)
     geo.cluster *= 2;
   geo.turn_slice0 = 0;
