@@ -141,7 +141,10 @@ attn_mass_kernel(const MassArgs a) {
 
 cudaError_t launch_attn_mass(const MassArgs& a, cudaStream_t stream) {
   const int smem = kCols * (int)sizeof(float) + kCols * q_row_bytes(a.d_c + a.d_rope);
-  cudaError_t e = cudaFuncSetAttribute(attn_mass_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  // always the most (rows of 512 + 256): calls of other sizes may be on their way from other
+  // host threads
+  cudaError_t e = cudaFuncSetAttribute(attn_mass_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       kCols * (int)sizeof(float) + kCols * q_row_bytes(768));
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr[1] = {pdl_attribute()};
   cudaLaunchConfig_t cfg = {};

@@ -467,7 +467,9 @@ cudaError_t launch(const CUtensorMap& tq, const CUtensorMap& tp, PairMassParams 
                    cudaStream_t stream) {
   prm.stages = Layout<NT, kKeys>::stages(prm.blocks);
   const int smem = Layout<NT, kKeys>::bytes(prm.blocks);
-  cudaError_t e = cudaFuncSetAttribute(attn_mass_pair_kernel<NT, kKeys>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  // always the most: calls of other sizes may be on their way from other host threads
+  cudaError_t e = cudaFuncSetAttribute(attn_mass_pair_kernel<NT, kKeys>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       kMaxSmem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2 * workers, 1, 1);
@@ -489,8 +491,9 @@ cudaError_t launch(const CUtensorMap& tq, const CUtensorMap& tp, PairMassParams 
 
 }  // namespace
 
-bool attn_mass_pair_supported(int row, int page_size) {
-  return row <= 64 * kMaxBlocks && page_size >= 8 && (page_size & (page_size - 1)) == 0;
+bool attn_mass_pair_supported(const MassArgs& a) {
+  return a.d_c + a.d_rope <= 64 * kMaxBlocks && a.page_size >= 8 && (a.page_size & (a.page_size - 1)) == 0 &&
+         (int64_t)a.num_pages * a.page_size < INT32_MAX;   // a load's coordinates are 32 bits, its row past the pool too
 }
 
 cudaError_t launch_attn_mass_pair(const MassArgs& a, int sms, long long spin_limit, cudaStream_t stream) {

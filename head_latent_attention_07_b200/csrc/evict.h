@@ -51,7 +51,7 @@ struct CompactArgs {
 bool encode_rows(CUtensorMap* m, const void* base, uint64_t rows, uint32_t width, uint32_t box_rows);
 
 // Tensor-core pairs (rows up to 576 wide, pages of a power of two), and any other shape.
-bool attn_mass_pair_supported(int row, int page_size);
+bool attn_mass_pair_supported(const MassArgs& a);
 cudaError_t launch_attn_mass_pair(const MassArgs& a, int sms, long long spin_limit, cudaStream_t stream);
 cudaError_t launch_attn_mass(const MassArgs& a, cudaStream_t stream);
 cudaError_t launch_evict_select(const SelectArgs& a, int sms, cudaStream_t stream);

@@ -11,7 +11,7 @@ namespace {
 
 constexpr int32_t kMaxNq = 1024;                 // the bounds of the decode calls, whose rows these are
 constexpr int64_t kMaxTokens = 1 << 18;
-constexpr int64_t kMaxLength = 1 << 30;          // tokens of one sequence in mla_evict_select
+constexpr int64_t kMaxLength = 1 << 30;          // tokens of one sequence: tiles past its end keep 32-bit indices
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
@@ -31,7 +31,7 @@ int check_cache_dims(const mla_dims* d) {
 
 int check_cache_shape(const mla_dims* d, int32_t batch, int32_t max_pages, int32_t num_pages) {
   if (batch < 1 || max_pages < 1 || num_pages < 1) return MLA_ERR_INVALID_ARG;
-  if (batch > mla::kMaxBatch || (int64_t)max_pages * d->page_size > INT32_MAX) return MLA_ERR_UNSUPPORTED;
+  if (batch > mla::kMaxBatch || (int64_t)max_pages * d->page_size > kMaxLength) return MLA_ERR_UNSUPPORTED;
   return MLA_OK;
 }
 
@@ -81,7 +81,7 @@ int mla_attn_mass(const mla_dims* dims, const mla_bf16* q_lat, const mla_bf16* p
   a.page_size = dims->page_size; a.max_pages = max_pages; a.num_pages = num_pages;
   a.scale = dims->softmax_scale > 0.f ? dims->softmax_scale : 1.0f / sqrtf((float)(dims->qk_nope + dims->d_rope));
   a.decay = decay;
-  if (!mla::attn_mass_pair_supported(a.d_c + a.d_rope, a.page_size))
+  if (!mla::attn_mass_pair_supported(a))
     return cuda_status(mla::launch_attn_mass(a, (cudaStream_t)stream));
   int sms = 0;
   if ((st = device_sms(&sms)) != MLA_OK) return st;

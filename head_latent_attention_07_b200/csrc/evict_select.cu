@@ -109,6 +109,7 @@ evict_select_kernel(const SelectArgs a, const int cluster, const int staged_max)
     for (int i = rank * threads + tid; i < len; i += cluster * threads) out[i] = i;
     return;
   }
+  if (cluster > 1) cluster_arrive_relaxed();             // answered before the first access to another CTA's memory
   const int first = min(a.n_sink, new_len);              // [0, first) stay
   const int last = len - min(a.n_recent, new_len - first);   // [last, len) stay
   uint32_t need = new_len - first - (len - last);        // of [first, last)
@@ -123,6 +124,7 @@ evict_select_kernel(const SelectArgs a, const int cluster, const int staged_max)
 #pragma unroll 8
   for (int i = begin + tid; i < begin + staged; i += threads) keys[i - begin] = mass_key(mass[i]);
   __syncthreads();
+  if (cluster > 1) cluster_wait();                       // every CTA has started
 
   // narrow [lo, hi] to the key of the last token that stays; `need` of the tokens in
   // it stay, and `whole` says that all of them do
@@ -258,7 +260,9 @@ cudaError_t launch_evict_select(const SelectArgs& a, int sms, cudaStream_t strea
   while (threads < kMaxThreads && threads * 8 < part) threads *= 2;
   const int staged = (int)(part < kMaxStaged ? part : kMaxStaged);
   const int smem = (int)((sizeof(SelectSmem) + 15) & ~size_t(15)) + staged * 4;
-  cudaError_t e = cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  // always the most: calls of other sizes may be on their way from other host threads
+  cudaError_t e = cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       (int)sizeof(SelectSmem) + 16 + kMaxStaged * 4);
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;

@@ -50,7 +50,7 @@
  *     sequence length outside the page table, a bounded wait that ran out) are
  *     recorded, first one wins, in the caller's int32 status word `dev_status`
  *     (may be NULL) and the offending access is skipped: no kernel traps.
- *   - Bounded waits: each wait between the roles of the decode kernels gives up
+ *   - Bounded waits: each wait between the roles of the decode and mass kernels gives up
  *     after about 2^31 cycles (~1 s), records MLA_ERR_TIMEOUT and ends the kernel
  *     cleanly.  The environment variable MLA_SPIN_LIMIT (cycles, read at each
  *     call) overrides the budget; tests set it small to exercise that path.
@@ -366,7 +366,9 @@ int mla_query_proj(const mla_dims* dims, int32_t q_lora_rank, const mla_bf16* h,
  * Sums are fp32, in an order that does not depend on the schedule.  A sequence
  * whose length is out of range (see mla_decode_attn) and the tokens of a page
  * outside the pool keep their mass; both record MLA_ERR_RANGE.  batch and nq as
- * for mla_decode_attn.
+ * for mla_decode_attn, max_pages * page_size <= 2^30 (else MLA_ERR_UNSUPPORTED).
+ * Rows up to 576 wide in pages of 8 to 256 tokens, a power of two, run on the
+ * tensor cores' pair instructions; other shapes on a slower kernel.
  */
 int mla_attn_mass(const mla_dims* dims, const mla_bf16* q_lat, const mla_bf16* pool, const int32_t* page_table,
                   const int32_t* seq_lens, const float* lse, int32_t batch, int32_t nq, int32_t max_pages,
@@ -424,7 +426,8 @@ int mla_evict_select(const float* mass, int64_t mass_stride, const int32_t* seq_
  * Rows with keep_idx[b][j] == j are not touched.  An index outside [j, seq_lens[b])
  * or a page outside the pool records MLA_ERR_RANGE and row j stays as it was; a
  * sequence whose lengths are out of range records it and is left alone.
- * batch <= 1024 and num_pages * page_size < 2^32 - 1 (else MLA_ERR_UNSUPPORTED).
+ * batch <= 1024, max_pages * page_size <= 2^30 and num_pages * page_size <
+ * 2^32 - 1 (else MLA_ERR_UNSUPPORTED).
  */
 int mla_cache_compact(const mla_dims* dims, mla_bf16* pool, const int32_t* page_table, const int32_t* seq_lens,
                       const int32_t* keep_idx, int64_t keep_stride, const int32_t* new_lens, int32_t batch,

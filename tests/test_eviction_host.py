@@ -56,6 +56,7 @@ def test_attn_mass_argument_checks(lib):
     assert call(nq=1025) == M.MLA_ERR_UNSUPPORTED
     assert call(B=1000, nq=1000) == M.MLA_ERR_UNSUPPORTED
     assert call(mp=1 << 26) == M.MLA_ERR_UNSUPPORTED
+    assert call(mp=(1 << 24) + 1, stride=1 << 40) == M.MLA_ERR_UNSUPPORTED     # longer than 2^30 tokens
 
 
 def test_evict_select_argument_checks(lib):
@@ -95,6 +96,7 @@ def test_cache_compact_argument_checks(lib):
         assert call(**bad) == M.MLA_ERR_INVALID_ARG, bad
     assert call(B=1025) == M.MLA_ERR_UNSUPPORTED
     assert call(mp=1 << 26) == M.MLA_ERR_UNSUPPORTED
+    assert call(np_=1 << 26) == M.MLA_ERR_UNSUPPORTED                          # row numbers past 32 bits
 
 
 # ------------------------------------------------------------------ the binding, on CPU tensors
