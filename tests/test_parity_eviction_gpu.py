@@ -303,6 +303,28 @@ def test_select_longer_than_shared_memory(kind):
     check_select(masses(kind, (150, 60000), 3), [60000 - 37 * b for b in range(150)], [1234] * 150, 4, 100)
 
 
+@pytest.mark.parametrize("batch", [1, 40])
+@pytest.mark.parametrize("equal", [1, 256, 700])
+def test_select_plateaus(equal, batch):
+    # equal masses spread over the CTAs; the border falls before, inside and behind them
+    n = 9000
+    g = np.random.default_rng([equal, batch])
+    m = np.exp(g.standard_normal((batch, n))).astype(np.float32)
+    for b in range(batch):
+        m[b, g.permutation(n)[:equal]] = 1.0
+    above = int((m[0] > 1.0).sum())
+    for k in (above, above + 1, above + equal // 2 + 1, above + equal, above + equal + 1):
+        check_select(m, [n] * batch, [k] * batch, 0, 0)
+        check_select(m, [n - 13 * b for b in range(batch)], [k] * batch, 5, 77)
+
+
+@pytest.mark.parametrize("n", [255, 256, 257, 513])
+def test_select_short_rows(n):
+    for kind in ("spread", "same", "anything"):
+        check_select(masses(kind, (3, n), n), [n, n - 1, n - 2], [n // 2, 1, n - 3], 0, 0)
+        check_select(masses(kind, (3, n), n), [n, n - 1, n - 2], [n // 2, 3, n - 3], 1, 1)
+
+
 def test_select_range_errors():
     m = masses("spread", (4, 100), 5)
     lens, budgets = [100, 101, 50, -1], [10, 10, -1, 10]
