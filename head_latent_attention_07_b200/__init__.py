@@ -125,9 +125,15 @@ def version() -> str:
 
 # ------------------------------------------------------------------ marshalling helpers
 
+_torch_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 def _ptr(t, dtype, name, ndim=None):
@@ -373,11 +379,14 @@ def mla_query_proj(dims: MlaDims, h, w_dq, w_uq, c_q, q, stream=None) -> None:
     _check(st, "mla_query_proj")
 
 
-def _pointers(*specs):
+def _pointers(stream, *specs):
     """Data pointers of (tensor, dtype, shape, name), None for an optional tensor that is
-    None.  Every tensor must be dense and on the current device, where the call launches."""
+    None, and last the stream's handle (the current one's for None).  Every tensor must be
+    dense and on the current device, where the call launches."""
+    torch = _torch()
     out = []
     device = None
+    refused = False
     try:
         for t, dtype, shape, _ in specs:
             if t is None:
@@ -385,15 +394,17 @@ def _pointers(*specs):
                 continue
             index = t.get_device()
             if device is None and index >= 0:
-                device = _torch().cuda.current_device()
+                device = torch.cuda.current_device()
             if t.dtype is not dtype or index != device or not t.is_contiguous() or (shape is not None and t.shape != shape):
+                refused = True
                 break
             out.append(t.data_ptr())
-        else:
-            return out
     except AttributeError:      # not a tensor
-        pass
-    _refuse(specs)
+        refused = True
+    if refused:
+        _refuse(specs)
+    out.append(torch._C._cuda_getCurrentRawStream(device) if stream is None else _stream(stream))
+    return out
 
 
 def _refuse(specs):
@@ -432,19 +443,19 @@ def mla_attn_mass(dims: MlaDims, q_lat, pool, page_table, seq_lens, lse, mass, m
     `decay` first.  lse [B, nq, H] is mla_decode_attn's."""
     torch = _torch()
     i32, f32, bf16 = torch.int32, torch.float32, torch.bfloat16
-    B, nq = q_lat.shape[0], q_lat.shape[1]
+    B, nq = q_lat.shape[:2]
     H, row, page = dims.n_heads, dims.row, dims.page_size
     max_pages = _matrix(page_table, B, "page_table")
     width = _matrix(mass, B, "mass")
     if width < max_pages * page:
         raise ValueError(f"mass rows must hold max_pages * page_size = {max_pages * page} tokens, got {width}")
     num_pages = pool.shape[0]
-    p = _pointers((q_lat, bf16, (B, nq, H, row), "q_lat"), (pool, bf16, (num_pages, page, row), "pool"),
+    p = _pointers(stream, (q_lat, bf16, (B, nq, H, row), "q_lat"), (pool, bf16, (num_pages, page, row), "pool"),
                   (page_table, i32, None, "page_table"), (seq_lens, i32, (B,), "seq_lens"),
                   (lse, f32, (B, nq, H), "lse"), (mass_lens, i32, (B,), "mass_lens"), (mass, f32, None, "mass"),
                   (dev_status, i32, None, "dev_status"))
     st = load_library().mla_attn_mass(ctypes.byref(dims), p[0], p[1], p[2], p[3], p[4], B, nq, max_pages, num_pages,
-                                      decay, p[5], p[6], width, p[7], _stream(stream))
+                                      decay, p[5], p[6], width, p[7], p[8])
     _check(st, "mla_attn_mass")
 
 
@@ -458,11 +469,11 @@ def mla_evict_select(mass, seq_lens, budgets, keep_idx, new_lens, n_sink: int = 
     if not (0 <= n_sink < 2**31 and 0 <= n_recent < 2**31):
         raise ValueError(f"n_sink and n_recent must be in [0, 2^31), got {n_sink}, {n_recent}")
     width, keep = _matrix(mass, B, "mass"), _matrix(keep_idx, B, "keep_idx")
-    p = _pointers((mass, torch.float32, None, "mass"), (seq_lens, i32, (B,), "seq_lens"),
+    p = _pointers(stream, (mass, torch.float32, None, "mass"), (seq_lens, i32, (B,), "seq_lens"),
                   (budgets, i32, (B,), "budgets"), (keep_idx, i32, None, "keep_idx"),
                   (new_lens, i32, (B,), "new_lens"), (dev_status, i32, None, "dev_status"))
     st = load_library().mla_evict_select(p[0], width, p[1], p[2], B, n_sink, n_recent, p[3], keep, p[4], p[5],
-                                         _stream(stream))
+                                         p[6])
     _check(st, "mla_evict_select")
 
 
@@ -478,12 +489,12 @@ def mla_cache_compact(dims: MlaDims, pool, page_table, seq_lens, keep_idx, new_l
     width = 0 if mass is None else _matrix(mass, B, "mass")
     if mass is not None and width < max_pages * page:
         raise ValueError(f"mass rows must hold max_pages * page_size = {max_pages * page} tokens, got {width}")
-    p = _pointers((pool, torch.bfloat16, (num_pages, page, dims.row), "pool"), (page_table, i32, None, "page_table"),
+    p = _pointers(stream, (pool, torch.bfloat16, (num_pages, page, dims.row), "pool"), (page_table, i32, None, "page_table"),
                   (seq_lens, i32, (B,), "seq_lens"), (keep_idx, i32, None, "keep_idx"),
                   (new_lens, i32, (B,), "new_lens"), (mass, torch.float32, None, "mass"),
                   (dev_status, i32, None, "dev_status"))
     st = load_library().mla_cache_compact(ctypes.byref(dims), p[0], p[1], p[2], p[3], keep, p[4], B, max_pages, num_pages,
-                                          1 if rerotate else 0, p[5], width, p[6], _stream(stream))
+                                          1 if rerotate else 0, p[5], width, p[6], p[7])
     _check(st, "mla_cache_compact")
 
 

@@ -133,7 +133,7 @@ int mla_cache_compact(const mla_dims* dims, mla_bf16* pool, const int32_t* page_
   const long double ratio = powl(theta, -2.0L / dims->d_rope);
   long double f = 1.0L / 6.283185307179586476925286766559L;
   for (int i = 0; i < dims->d_rope / 2; ++i, f *= ratio)
-    a.turn[i] = (uint64_t)((f - floorl(f)) * 18446744073709551616.0L);
+    a.turn[i] = (uint64_t)((f >= 1.0L ? f - floorl(f) : f) * 18446744073709551616.0L);
   return cuda_status(mla::launch_cache_compact(a, sms, (cudaStream_t)stream));
 }
 
