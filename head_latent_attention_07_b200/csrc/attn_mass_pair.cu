@@ -32,7 +32,6 @@
 
 #include "common.cuh"
 #include "evict.h"
-#include "plan.cuh"
 #include "sm100.cuh"
 
 namespace mla {
@@ -78,7 +77,6 @@ struct Bars {
   uint64_t drain;        // both: every MMA issued has completed
   uint32_t tmem_base;
   int abort;
-  int b0, tile0;         // where this worker starts
 };
 static_assert(Layout<256, false>::kOffBar + sizeof(Bars) <= Layout<256, false>::kOffRes, "barrier area");
 
@@ -99,6 +97,43 @@ __device__ __forceinline__ int seq_tiles(const MassArgs& a, int b, int* len) {
   return *len < a.nq || *len > a.max_pages * a.page_size ? 0 : (*len + kTileKeys - 1) / kTileKeys;
 }
 
+// Worker w's share of the tiles: those of all sequences end to end, in equal parts.  Each
+// warp finds it by itself (two passes over the lengths, 32 at a time), so that the start
+// needs no barrier after the lengths are known.
+struct Share {
+  int b, tile, count;    // first sequence, first tile, tiles
+};
+__device__ __forceinline__ Share find_share(const MassArgs& a, int w, int workers, int lane) {
+  auto tiles_of = [&](int b) {
+    int len;
+    return b < a.batch ? seq_tiles(a, b, &len) : 0;
+  };
+  int total = 0;
+  for (int base = 0; base < a.batch; base += 32) total += __reduce_add_sync(0xffffffffu, tiles_of(base + lane));
+  const int t0 = (int)((long long)total * w / workers);
+  Share s = {0, 0, (int)((long long)total * (w + 1) / workers) - t0};
+  int carry = 0;
+  for (int base = 0; base < a.batch && s.count > 0; base += 32) {
+    const int v = tiles_of(base + lane);
+    int end = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, end, o);
+      if (lane >= o) end += y;
+    }
+    end += carry;
+    const uint32_t hit = __ballot_sync(0xffffffffu, end - v <= t0 && t0 < end);
+    if (hit != 0) {
+      const int at = __ffs(hit) - 1;
+      s.b = base + at;
+      s.tile = t0 - __shfl_sync(0xffffffffu, end - v, at);
+      break;
+    }
+    carry = __shfl_sync(0xffffffffu, end, 31);
+  }
+  return s;
+}
+
 // One accumulator's worth of work; every role walks the same ones in the same order.
 struct Item {
   int b, len, tile, group;
@@ -109,7 +144,7 @@ struct Cursor {
   const PairMassParams& p;
   int b, tile, left;     // next sequence and tile, tiles left of this worker's share
   int len = 0, sub0 = 0, sub1 = 0, t = 0, g = 0;
-  __device__ Cursor(const PairMassParams& p_, const Bars* bar, int share) : p(p_), b(bar->b0), tile(bar->tile0), left(share) {}
+  __device__ Cursor(const PairMassParams& p_, const Share& s) : p(p_), b(s.b), tile(s.tile), left(s.count) {}
   __device__ bool next(Item* it) {
     // through the groups of a tile (kKeys), or through the tiles [sub0, sub1) of a group
     bool done;
@@ -198,41 +233,19 @@ attn_mass_pair_kernel(const __grid_constant__ CUtensorMap tq, const __grid_const
     tmem_alloc_pair(&bar->tmem_base, 2 * NT);
     tmem_relinquish_pair();
   }
-  grid_dependency_wait();
-  allow_dependent_launch();
-
-  // the tiles of all sequences end to end, an equal share for each worker: where
-  // does this one's start?  (lse2 serves as scratch)
-  int total = 0, share = 0;
-  {
-    int* scratch = reinterpret_cast<int*>(lse2);
-    for (int base = 0; base < a.batch; base += kThreads) {
-      const int b = base + threadIdx.x;
-      int len, tot;
-      const int v = b < a.batch ? seq_tiles(a, b, &len) : 0;
-      if (b < a.batch && v == 0 && blockIdx.x == 0) record_status(status, MLA_ERR_RANGE);
-      block_exclusive_scan(v, scratch, &tot);
-      total += tot;
-    }
-    const int t0 = (int)((long long)total * w / workers);
-    share = (int)((long long)total * (w + 1) / workers) - t0;
-    int carry = 0;
-    for (int base = 0; base < a.batch && carry <= t0; base += kThreads) {
-      const int b = base + threadIdx.x;
-      int len, tot;
-      const int v = b < a.batch ? seq_tiles(a, b, &len) : 0;
-      const int at = carry + block_exclusive_scan(v, scratch, &tot);
-      if (v > 0 && at <= t0 && t0 < at + v) {
-        bar->b0 = b;
-        bar->tile0 = t0 - at;
-      }
-      carry += tot;
-    }
-  }
   __syncthreads();
   tc_fence_before();
   cluster_sync();        // barriers and TMEM of both CTAs ready before any remote traffic
   tc_fence_after();
+  // setup above touches no input: the predecessor on the stream may still run
+  grid_dependency_wait();
+  allow_dependent_launch();
+  if (blockIdx.x == 0) {
+    int len;
+    for (int b = threadIdx.x; b < a.batch; b += kThreads)
+      if (seq_tiles(a, b, &len) == 0) record_status(status, MLA_ERR_RANGE);
+  }
+  const Share share = find_share(a, w, workers, lane);
   const uint32_t tmem = bar->tmem_base;
   auto wwait = [&](uint64_t* b, uint32_t parity) -> bool {
     return __all_sync(0xffffffffu, mbar_wait(b, parity, abort_flag, status, lim));
@@ -250,7 +263,7 @@ attn_mass_pair_kernel(const __grid_constant__ CUtensorMap tq, const __grid_const
     const int n_boxes = 128 / prm.box_rows, box_bytes = prm.box_rows * 128;
     const bool has_box = lane < n_boxes;
     const int box_key = (int)c * 128 + lane * prm.box_rows;      // its first key within a tile
-    Cursor<kKeys> cur(prm, bar, share);
+    Cursor<kKeys> cur(prm, share);
     Item next;
     int next_id = 0;
     auto fetch = [&]() -> bool {
@@ -306,7 +319,7 @@ attn_mass_pair_kernel(const __grid_constant__ CUtensorMap tq, const __grid_const
     if (c == 0) {
       const uint32_t idesc = idesc_bf16_f32(256, NT, 0, 0);
       const uint32_t res = smem_u32(res_s), ring = smem_u32(ring_s);
-      Cursor<kKeys> cur(prm, bar, share);
+      Cursor<kKeys> cur(prm, share);
       Item it;
       int s = 0, ri = -1, t = 0;
       uint32_t lap = 0;
@@ -344,7 +357,7 @@ attn_mass_pair_kernel(const __grid_constant__ CUtensorMap tq, const __grid_const
     __syncwarp();
   } else if (warp == 2) {
     // ------------------------------------------------------------ lse of a group's query rows
-    Cursor<kKeys> cur(prm, bar, share);
+    Cursor<kKeys> cur(prm, share);
     Item it;
     int gi = 0;
     while (cur.next(&it)) {
@@ -372,7 +385,7 @@ attn_mass_pair_kernel(const __grid_constant__ CUtensorMap tq, const __grid_const
     const int row = (int)c * 128 + (warp & 3) * 32 + lane;   // this thread's key within a tile
     // The key's page id and its mass so far are fetched an item ahead: their latency would
     // otherwise add to each tile's sum.
-    Cursor<kKeys> cur(prm, bar, share);
+    Cursor<kKeys> cur(prm, share);
     Item next;
     int next_id = -1;
     float next_mass = 0.f;
