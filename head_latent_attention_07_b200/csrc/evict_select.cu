@@ -42,9 +42,12 @@ struct SelectSmem {
   uint32_t found_bin, found_above, found_count;   // the bin of the wanted rank
 };
 
-// Unsigned key in the order of the value: larger mass, larger key.
+// Unsigned key in the order of the value: larger mass, larger key.  The smallest is
+// -infinity's 0x007FFFFF; below lie kNoKey, for places past the end, and kNoTie; above
+// all, the key of a token that stays whatever its mass.
+constexpr uint32_t kNoKey = 0, kNoTie = 1, kNanKey = 0xFFFFFFFEu, kStays = 0xFFFFFFFFu;
 __device__ __forceinline__ uint32_t mass_key(float v) {
-  if (isnan(v)) return 0xFFFFFFFFu;
+  if (isnan(v)) return kNanKey;
   const uint32_t u = __float_as_uint(v == 0.f ? 0.f : v);
   return (u & 0x80000000u) ? ~u : u | 0x80000000u;
 }
@@ -114,31 +117,41 @@ evict_select_kernel(const SelectArgs a, const int cluster, const int staged_max)
   const int last = len - min(a.n_recent, new_len - first);   // [last, len) stay
   uint32_t need = new_len - first - (len - last);        // of [first, last)
 
-  // this CTA's part: whole 32-token groups, in order over the ranks
-  const int part = ((len + cluster - 1) / cluster + 31) & ~31;
+  // this CTA's part: whole groups of 128 tokens (four for each lane of a warp), in order over
+  // the ranks
+  const int part = ((len + cluster - 1) / cluster + 127) & ~127;
   const int begin = min(rank * part, len), end = min(begin + part, len);
-  const int staged = min(end - begin, staged_max);
+  const int staged = min((end - begin + 127) & ~127, staged_max);
   const float* mass = a.mass + (size_t)b * a.mass_stride;
-  auto key_at = [&](int i) { return i - begin < staged ? keys[i - begin] : mass_key(mass[i]); };
+  auto key_of = [&](int i) {
+    return i >= end ? kNoKey : i < first || i >= last ? kStays : mass_key(mass[i]);
+  };
+  auto quad_at = [&](int i) {                            // the keys of four tokens, i - begin a multiple of 4
+    return i - begin < staged ? *reinterpret_cast<const uint4*>(keys + (i - begin))
+                              : make_uint4(key_of(i), key_of(i + 1), key_of(i + 2), key_of(i + 3));
+  };
 
 #pragma unroll 8
-  for (int i = begin + tid; i < begin + staged; i += threads) keys[i - begin] = mass_key(mass[i]);
+  for (int i = tid; i < staged; i += threads) keys[i] = key_of(begin + i);
   __syncthreads();
   if (cluster > 1) cluster_wait();                       // every CTA has started
 
   // narrow [lo, hi] to the key of the last token that stays; `need` of the tokens in
   // it stay, and `whole` says that all of them do
   bool whole = false;
-  uint32_t lo = 0, hi = 0xFFFFFFFFu;
+  uint32_t lo = kNoTie + 1, hi = kNanKey;
   for (int round = 0; need > 0 && !whole && lo < hi; ++round) {
     // bin i holds the keys from base + (i << shift) on, the first and the last all beyond
     const int shift = round == 0 ? kFirstShift : max(0, 21 - __clz(hi - lo));   // (hi - lo) >> shift < kBins
     const uint32_t base = round == 0 ? kFirstLo : lo;
     uint32_t* hist = sm->hist[round & 1];
-#pragma unroll 4
-    for (int i = max(begin, first) + tid; i < min(end, last); i += threads) {
-      const uint32_t k = key_at(i);
+    auto count = [&](uint32_t k) {
       if (k >= lo && k <= hi) atomicAdd(&hist[k < base ? 0 : min((k - base) >> shift, kBins - 1u)], 1u);
+    };
+#pragma unroll 2
+    for (int i = begin + 4 * tid; i < end; i += 4 * threads) {
+      const uint4 q = quad_at(i);
+      count(q.x), count(q.y), count(q.z), count(q.w);
     }
     __syncthreads();
     for (int g = warp; g < kGroups; g += warps) {
@@ -177,34 +190,23 @@ evict_select_kernel(const SelectArgs a, const int cluster, const int staged_max)
     if (bin < kBins - 1u) hi = from + min(hi - from, (1u << shift) - 1u);
     if (bin > 0) lo = from;
   }
-  // keys above hi stay; of those in [lo, hi]: all when `whole`, else (lo == hi) the
-  // first `need`
-  const bool none = need == 0;
-  auto classify = [&](int i, bool* stays, bool* tie) {
-    *stays = false;
-    *tie = false;
-    if (i >= end) return;
-    if (i < first || i >= last) { *stays = true; return; }
-    if (none) return;
-    const uint32_t k = key_at(i);
-    *stays = whole ? k >= lo : k > hi;
-    *tie = !whole && k == hi;
-  };
+  // keys above `over` stay, and of those equal to `tie` the first `need`: of the keys in
+  // [lo, hi] all when `whole`, else (lo == hi) the first ones
+  const uint32_t over = need == 0 ? kNanKey : whole ? lo - 1 : hi;
+  const uint32_t tie = need == 0 || whole ? kNoTie : hi;
 
   // each warp's place: counts of the lower ranks, then of the lower warps
-  const int per_warp = ((end - begin + warps - 1) / warps + 31) & ~31;
+  const int per_warp = ((end - begin + warps - 1) / warps + 127) & ~127;
   const int wb = min(begin + warp * per_warp, end), we = min(wb + per_warp, end);
   uint32_t n_stay = 0, n_tie = 0;
-  uint32_t my_stay = 0, my_tie = 0;                      // lane l: the ballots of the warp's l-th group
-#pragma unroll 4
-  for (int i = wb; i < we; i += 32) {
-    bool stays, tie;
-    classify(i + lane, &stays, &tie);
-    const uint32_t sb = __ballot_sync(0xffffffffu, stays), tb = __ballot_sync(0xffffffffu, tie);
-    if (i - wb == lane * 32) { my_stay = sb; my_tie = tb; }
-    n_stay += __popc(sb);
-    n_tie += __popc(tb);
+#pragma unroll 2
+  for (int i = wb + 4 * lane; i < we; i += 128) {
+    const uint4 q = quad_at(i);
+    n_stay += (q.x > over) + (q.y > over) + (q.z > over) + (q.w > over);
+    n_tie += (q.x == tie) + (q.y == tie) + (q.z == tie) + (q.w == tie);
   }
+  n_stay = __reduce_add_sync(0xffffffffu, n_stay);
+  n_tie = __reduce_add_sync(0xffffffffu, n_tie);
   if (lane == 0) { sm->warp_a[warp] = n_stay; sm->warp_b[warp] = n_tie; }
   __syncthreads();
   const uint32_t s = warp_inclusive(lane < warps ? sm->warp_a[lane] : 0, lane);
@@ -225,24 +227,26 @@ evict_select_kernel(const SelectArgs a, const int cluster, const int staged_max)
       tie0 += sm->ties[r];
     }
   }
-  const uint32_t below = (1u << lane) - 1u;
-#pragma unroll 4
-  for (int i = wb; i < we; i += 32) {
-    uint32_t sb, tb;
-    if (i - wb < 32 * 32) {
-      sb = __shfl_sync(0xffffffffu, my_stay, (i - wb) >> 5);
-      tb = __shfl_sync(0xffffffffu, my_tie, (i - wb) >> 5);
-    } else {
-      bool stays, tie;
-      classify(i + lane, &stays, &tie);
-      sb = __ballot_sync(0xffffffffu, stays);
-      tb = __ballot_sync(0xffffffffu, tie);
+#pragma unroll 2
+  for (int i0 = wb; i0 < we; i0 += 128) {
+    const int i = i0 + 4 * lane;
+    const uint4 q = quad_at(i);
+    const uint32_t k[4] = {q.x, q.y, q.z, q.w};
+    uint32_t mine = 0;                                   // what stays, and the ties in the upper half
+#pragma unroll
+    for (int e = 0; e < 4; ++e) mine += (k[e] > over ? 1u : 0u) + (k[e] == tie ? 0x10000u : 0u);
+    const uint32_t incl = warp_inclusive(mine, lane), before = incl - mine;
+    uint32_t stay = stay0 + (before & 0xFFFFu), ties = tie0 + (before >> 16);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const bool is_tie = k[e] == tie;
+      if (k[e] > over || (is_tie && ties < need)) out[stay + min(ties, need)] = i + e;
+      stay += k[e] > over;
+      ties += is_tie;
     }
-    const uint32_t ties_before = tie0 + __popc(tb & below);
-    if ((sb >> lane & 1u) || ((tb >> lane & 1u) && ties_before < need))
-      out[stay0 + __popc(sb & below) + min(ties_before, need)] = i + lane;
-    stay0 += __popc(sb);
-    tie0 += __popc(tb);
+    const uint32_t all = __shfl_sync(0xffffffffu, incl, 31);
+    stay0 += all & 0xFFFFu;
+    tie0 += all >> 16;
   }
 }
 
@@ -255,7 +259,7 @@ cudaError_t launch_evict_select(const SelectArgs& a, int sms, cudaStream_t strea
   int cluster = 1;
   while (cluster < kMaxCluster && (int64_t)2 * cluster * a.batch <= sms && a.mass_stride > (int64_t)2048 * cluster)
     cluster *= 2;
-  const int64_t part = ((a.mass_stride + cluster - 1) / cluster + 31) & ~int64_t(31);
+  const int64_t part = ((a.mass_stride + cluster - 1) / cluster + 127) & ~int64_t(127);
   int threads = 512;
   while (threads < kMaxThreads && threads * 8 < part) threads *= 2;
   const int staged = (int)(part < kMaxStaged ? part : kMaxStaged);
