@@ -27,7 +27,7 @@ namespace {
 
 using namespace sm100;
 
-constexpr int kMaxThreads = 1024;
+constexpr int kMinThreads = 512, kMaxThreads = 1024;
 constexpr int kBins = 2048, kGroups = kBins / 32;
 constexpr int kFirstShift = 17;
 constexpr uint32_t kFirstLo = 0x80000000u | ((127u - 24u) << 23);   // key of 2^-24
@@ -123,16 +123,25 @@ evict_select_kernel(const SelectArgs a, const int cluster, const int staged_max)
   const int begin = min(rank * part, len), end = min(begin + part, len);
   const int staged = min((end - begin + 127) & ~127, staged_max);
   const float* mass = a.mass + (size_t)b * a.mass_stride;
-  auto key_of = [&](int i) {
-    return i >= end ? kNoKey : i < first || i >= last ? kStays : mass_key(mass[i]);
-  };
+  auto key_for = [&](int i, float v) { return i >= end ? kNoKey : i < first || i >= last ? kStays : mass_key(v); };
+  auto key_of = [&](int i) { return key_for(i, i < end ? mass[i] : 0.f); };
   auto quad_at = [&](int i) {                            // the keys of four tokens, i - begin a multiple of 4
     return i - begin < staged ? *reinterpret_cast<const uint4*>(keys + (i - begin))
                               : make_uint4(key_of(i), key_of(i + 1), key_of(i + 2), key_of(i + 3));
   };
 
-#pragma unroll 8
-  for (int i = tid; i < staged; i += threads) keys[i] = key_of(begin + i);
+  constexpr int kLoads = 8;                              // in flight at a time
+  for (int i0 = tid; i0 < staged; i0 += kLoads * threads) {
+    float v[kLoads];
+#pragma unroll
+    for (int e = 0; e < kLoads; ++e) {
+      const int i = begin + i0 + e * threads;
+      v[e] = i < end ? mass[i] : 0.f;
+    }
+#pragma unroll
+    for (int e = 0; e < kLoads; ++e)
+      if (i0 + e * threads < staged) keys[i0 + e * threads] = key_for(begin + i0 + e * threads, v[e]);
+  }
   __syncthreads();
   if (cluster > 1) cluster_wait();                       // every CTA has started
 
@@ -154,9 +163,16 @@ evict_select_kernel(const SelectArgs a, const int cluster, const int staged_max)
       count(q.x), count(q.y), count(q.z), count(q.w);
     }
     __syncthreads();
-    for (int g = warp; g < kGroups; g += warps) {
-      const uint32_t v = __reduce_add_sync(0xffffffffu, hist[g * 32 + lane]);
-      if (lane < cluster) st_remote(mapa(smem_u32(&sm->coarse[rank][g]), lane), v);
+    uint32_t sum[kGroups / (kMinThreads / 32)];
+#pragma unroll
+    for (int j = 0; j < kGroups / (kMinThreads / 32); ++j) {
+      const int g = warp + j * warps;
+      sum[j] = __reduce_add_sync(0xffffffffu, g < kGroups ? hist[g * 32 + lane] : 0);
+    }
+#pragma unroll
+    for (int j = 0; j < kGroups / (kMinThreads / 32); ++j) {
+      const int g = warp + j * warps;
+      if (g < kGroups && lane < cluster) st_remote(mapa(smem_u32(&sm->coarse[rank][g]), lane), sum[j]);
     }
     sync();
     // the other counts were read before this barrier
@@ -164,18 +180,26 @@ evict_select_kernel(const SelectArgs a, const int cluster, const int staged_max)
     if (warp == 0) {
       // from the top: the pair of groups, the group, then the bin with the wanted rank
       uint32_t c[2] = {0, 0}, v = 0, above, in_pair, in_group;
-      for (int r = 0; r < cluster; ++r) {
-        c[0] += sm->coarse[r][kGroups - 1 - 2 * lane];
-        c[1] += sm->coarse[r][kGroups - 2 - 2 * lane];
+#pragma unroll
+      for (int r = 0; r < kMaxCluster; ++r) {
+        c[0] += r < cluster ? sm->coarse[r][kGroups - 1 - 2 * lane] : 0;
+        c[1] += r < cluster ? sm->coarse[r][kGroups - 2 - 2 * lane] : 0;
       }
       const int pair = lane_of_rank(c[0] + c[1], need, lane, &above);
       in_pair = __shfl_sync(0xffffffffu, c[0], pair);
       const bool second = above + in_pair < need;
       if (second) above += in_pair;
       const int bin0 = (kGroups - 1 - 2 * pair - (second ? 1 : 0)) * 32;
+      if (cluster > 1) {
+        uint32_t of[kMaxCluster];                        // all on their way before the first is used
 #pragma unroll
-      for (int r = 0; r < kMaxCluster; ++r)
-        if (r < cluster) v += ld_remote(mapa(smem_u32(&hist[bin0 + 31 - lane]), r));
+        for (int r = 0; r < kMaxCluster; ++r)
+          of[r] = ld_remote(mapa(smem_u32(&hist[bin0 + 31 - lane]), min(r, cluster - 1)));
+#pragma unroll
+        for (int r = 0; r < kMaxCluster; ++r) v += r < cluster ? of[r] : 0;
+      } else {
+        v = hist[bin0 + 31 - lane];
+      }
       const int at = lane_of_rank(v, need - above, lane, &in_group);
       if (lane == at) {
         sm->found_bin = bin0 + 31 - at;
@@ -255,12 +279,12 @@ evict_select_kernel(const SelectArgs a, const int cluster, const int staged_max)
 cudaError_t launch_evict_select(const SelectArgs& a, int sms, cudaStream_t stream) {
   // CTAs per sequence: as many as give each about 2048 tokens, while all fit the GPU.
   // 64 sequences of up to 65536 took 71, 32 and 40 us with clusters of 1, 2 and 4 of 1024
-  // threads; 16 of 32768 took 13.6 and 14.7 us with 4 of 1024 and 8 of 512.
+  // threads; 16 of 32768 took 18, 13.5 and 14.2 us with 2 and 4 of 1024 and 8 of 512.
   int cluster = 1;
   while (cluster < kMaxCluster && (int64_t)2 * cluster * a.batch <= sms && a.mass_stride > (int64_t)2048 * cluster)
     cluster *= 2;
   const int64_t part = ((a.mass_stride + cluster - 1) / cluster + 127) & ~int64_t(127);
-  int threads = 512;
+  int threads = kMinThreads;
   while (threads < kMaxThreads && threads * 8 < part) threads *= 2;
   const int staged = (int)(part < kMaxStaged ? part : kMaxStaged);
   const int smem = (int)((sizeof(SelectSmem) + 15) & ~size_t(15)) + staged * 4;
