@@ -175,6 +175,19 @@ def test_mass_rows_without_keys_and_masked_garbage(shape):
     assert np.array_equal(again, got)
 
 
+@pytest.mark.parametrize("shape", [(512, 64), (64, 16), (24, 16, 7)])
+@pytest.mark.parametrize("nq,heads", [(1, 5), (3, 100)])
+def test_mass_of_one_sequence_is_not_touched_by_another(shape, nq, heads):
+    # NaN in the queries of a sequence, whose rows lie behind its neighbour's in memory
+    c = Cache([100, 333, 70], nq, heads, *shape, seed=12).make_lse()
+    want = c.run()
+    c.q[1] = float("nan")
+    c.mass = torch.from_numpy(c.mass0).cuda()
+    got = c.run()
+    assert np.isnan(got[1, :333]).all()
+    assert np.array_equal(got[[0, 2]], want[[0, 2]]) and np.array_equal(got[1, 333:], want[1, 333:])
+
+
 def test_mass_large_scores():
     # scores far from each other: weights from 1 down to nothing
     check_mass(Cache([500, 64], 1, 128, seed=6, spread=4.0).make_lse())
@@ -277,7 +290,7 @@ def masses(kind, shape, seed):
 @pytest.mark.parametrize("lens,budgets,sink,recent", [
     ([1000], [500], 4, 64), ([1, 2, 33], [1, 1, 32], 0, 0), ([31, 32, 33, 0, 64], [7, 31, 32, 5, 0], 2, 3),
     ([2047, 2049, 4096, 5001], [100, 2048, 4095, 1], 1, 33), ([9000, 70, 12000], [8999, 500, 3], 16, 256),
-    ([20000, 131], [64, 130], 4, 4096),
+    ([20000, 131], [64, 130], 4, 4096), ([3000, 9], [70, 8], 2**31 - 1, 2**31 - 1), ([3000, 9], [70, 8], 0, 2**31 - 1),
 ])
 def test_select(kind, lens, budgets, sink, recent):
     check_select(masses(kind, (len(lens), max(lens)), len(lens)), lens, budgets, sink, recent)
