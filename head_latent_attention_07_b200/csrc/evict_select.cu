@@ -16,7 +16,8 @@
 //
 // Latency binds it (2 MB of mass are read in well under a microsecond): one cluster
 // barrier a round, which the counts of groups of bins cross; the bins of the one group that
-// matters are read from the other CTAs' shared memory after it.
+// matters are read from the other CTAs' shared memory after it.  Measured: 4.5 us for 1000
+// tokens, 12.0 for 16 x 32768, 17 for 8 x 131072 (the mass itself at 0.25 TB/s).
 #include "common.cuh"
 #include "evict.h"
 #include "sm100.cuh"
@@ -277,11 +278,21 @@ evict_select_kernel(const SelectArgs a, const int cluster, const int staged_max)
 }  // namespace
 
 cudaError_t launch_evict_select(const SelectArgs& a, int sms, cudaStream_t stream) {
-  // CTAs per sequence: as many as give each about 2048 tokens, while all fit the GPU.
-  // 64 sequences of up to 65536 took 71, 32 and 40 us with clusters of 1, 2 and 4 of 1024
-  // threads; 16 of 32768 took 18, 13.5 and 14.2 us with 2 and 4 of 1024 and 8 of 512.
+  // CTAs per sequence: as many as give each about 2048 tokens, while every CTA has an SM of
+  // its own.  Clusters of 8 do not pack onto all SMs: 12 of them ran at once on 148, 16 in
+  // two waves (of 1024 threads) or two to an SM (of 512), so they may take two thirds.
+  // Threads: 8 tokens each before the block doubles.  GPU time, us, by cluster x threads:
+  //   16 x 2048     1 x 512  5.9    2 x 512  7.1
+  //   16 x 8192     1 x 1024 10.4   2 x 512  8.7    4 x 512  7.7    8 x 512  9.1
+  //    8 x 16384                    4 x 512  9.0    8 x 512  8.3
+  //   12 x 32768                    4 x 1024 11.9   8 x 512  9.9
+  //   16 x 32768    2 x 1024 16.1   4 x 1024 12.1   8 x 512 12.4    8 x 1024 20.4
+  //   16 x 65536                    4 x 1024 16.4   8 x 512 16.6    8 x 1024 24.2
+  //    8 x 131072                   4 x 1024 24.3   8 x 512 18.4    8 x 1024 17.0
+  //   64 ragged to 65536   1 x 1024 53.9   2 x 512 30.7   2 x 1024 26.8   4 x 1024 33.1
   int cluster = 1;
-  while (cluster < kMaxCluster && (int64_t)2 * cluster * a.batch <= sms && a.mass_stride > (int64_t)2048 * cluster)
+  while (cluster < kMaxCluster && a.mass_stride > (int64_t)2048 * cluster &&
+         (int64_t)2 * cluster * a.batch <= (2 * cluster < kMaxCluster ? sms : sms * 2 / 3))
     cluster *= 2;
   const int64_t part = ((a.mass_stride + cluster - 1) / cluster + 127) & ~int64_t(127);
   int threads = kMinThreads;
