@@ -11,11 +11,14 @@
 //
 // One CTA takes 128 keys of a sequence, 16 per warp, and walks the nq * H query
 // rows in blocks of 64 columns, each staged in shared memory.  The key rows go from
-// global memory straight into fragments (16-byte pieces, see mma_frag.cuh).
+// global memory straight into fragments (16-byte pieces, see mma_frag.cuh), two slices ahead
+// of their products, and are read again from L2 for every block.
 //
-// The mma.sync pipe binds it, with the staged rows' shared-memory reads: 16 x 32768 tokens
-// 640 wide take 848 us at 128 heads (101 TFLOP/s) and 260 us at 16 (2.6 TB/s).  It is for the
-// shapes that the CTA-pair kernel does not take: rows over 576, other page sizes.
+// Latency binds it, of the keys' loads and of the staging, at 16 warps per SM: 16 x 32768
+// tokens 640 wide take 490 us at 128 heads (175 TFLOP/s) and 173 us at 16 (3.9 TB/s).  With
+// each slice loaded when it was needed it was 848 and 260 us, with the query rows staged
+// through registers 551 and 181.  It is for the shapes that the CTA-pair kernel does not
+// take: rows over 576, other page sizes.
 #include "common.cuh"
 #include "evict.h"
 #include "mma_frag.cuh"
@@ -28,11 +31,18 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kKeys = 128;       // keys per CTA, 16 per warp
 constexpr int kCols = 64;        // query rows per block
+constexpr int kAhead = 2;        // 32-column slices of the keys on their way (4 spill registers)
 constexpr float kLog2e = 1.4426950408889634f;
 
 // Bytes of one staged query row: whole 32-column slices, and 64 bytes modulo 128,
 // so that the 16-byte reads of two neighbouring rows fall into different banks.
 __host__ __device__ inline int q_row_bytes(int row) { return (row * 2 + 127) / 128 * 128 + 64; }
+
+// 16 bytes from src to shared memory, or zeros (`any` is then a valid address, not read)
+__device__ __forceinline__ void cp_async16_or_zero(uint32_t dst, const void* src, const void* any, bool in) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(in ? src : any), "r"(in ? 16 : 0)
+               : "memory");
+}
 
 __global__ void __launch_bounds__(kThreads)
 attn_mass_kernel(const MassArgs a) {
@@ -41,6 +51,7 @@ attn_mass_kernel(const MassArgs a) {
   unsigned char* q_s = smem + kCols * sizeof(float);       // [kCols][q_row_bytes]
   const int R = a.d_c + a.d_rope;
   const int rv = R / 8;                                    // 16-byte pieces per row
+  const uint32_t q_dst = sm100::smem_u32(q_s);
   const int slices = (R + 31) / 32;
   const int q_bytes = q_row_bytes(R);
   const int rows_total = a.nq * a.n_heads;
@@ -78,15 +89,21 @@ attn_mass_kernel(const MassArgs a) {
   for (int c0 = 0; c0 < rows_total; c0 += kCols) {
     const int cols = min(kCols, rows_total - c0);
     const int tiles = (cols + 7) >> 3;
+    // the pieces of the next kAhead slices are on their way while these are multiplied
+    uint4 ahead[kAhead][2];
+    auto fetch = [&](int s, uint4 (&r)[2]) {
+      const int v = s * 4 + quad;
+#pragma unroll
+      for (int j = 0; j < 2; ++j) r[j] = src[j] != nullptr && v < rv ? src[j][v] : make_uint4(0, 0, 0, 0);
+    };
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) fetch(k, ahead[k]);
     if (c0 > 0) __syncthreads();                           // the previous block has been read
     const uint16_t* qb = a.q_lat + ((size_t)b * rows_total + c0) * R;
     const int per_row = slices * 4;                        // pieces per staged row, zeros past R
-    for (int idx = threadIdx.x; idx < tiles * 8 * per_row; idx += kThreads) {
-      const int c = idx / per_row, v = idx % per_row;
-      uint4 u = make_uint4(0, 0, 0, 0);
-      if (c < cols && v < rv) u = *reinterpret_cast<const uint4*>(qb + (size_t)c * R + v * 8);
-      *reinterpret_cast<uint4*>(q_s + c * q_bytes + v * 16) = u;
-    }
+    for (int c = warp; c < tiles * 8; c += kThreads / 32)
+      for (int v = lane; v < per_row; v += 32)
+        cp_async16_or_zero(q_dst + c * q_bytes + v * 16, qb + (size_t)c * R + v * 8, qb, c < cols && v < rv);
     if (threadIdx.x < kCols) {
       // a row that saw no key (lse = -inf) gives nothing: exp2(x - inf) = 0
       float l = INFINITY;
@@ -96,6 +113,7 @@ attn_mass_kernel(const MassArgs a) {
       }
       lse2[threadIdx.x] = l;
     }
+    asm volatile("cp.async.wait_all;" ::: "memory");
     __syncthreads();
 
     float acc[8][4];
@@ -103,16 +121,18 @@ attn_mass_kernel(const MassArgs a) {
     for (int t = 0; t < 8; ++t)
 #pragma unroll
       for (int k = 0; k < 4; ++k) acc[t][k] = 0.f;
-#pragma unroll 4
-    for (int s = 0; s < slices; ++s) {
-      const int v = s * 4 + quad;
-      const uint4 zero = make_uint4(0, 0, 0, 0);
-      const uint4 ra = src[0] != nullptr && v < rv ? src[0][v] : zero;
-      const uint4 rb = src[1] != nullptr && v < rv ? src[1][v] : zero;
+    for (int s0 = 0; s0 < slices; s0 += kAhead) {
 #pragma unroll
-      for (int t = 0; t < 8; ++t)
-        if (t < tiles)
-          mma_k32(acc[t], ra, rb, *reinterpret_cast<const uint4*>(q_s + (t * 8 + g) * q_bytes + v * 16));
+      for (int k = 0; k < kAhead; ++k) {
+        if (s0 + k < slices) {
+          const uint4 ra = ahead[k][0], rb = ahead[k][1];
+          fetch(s0 + k + kAhead, ahead[k]);
+#pragma unroll
+          for (int t = 0; t < 8; ++t)
+            if (t < tiles)
+              mma_k32(acc[t], ra, rb, *reinterpret_cast<const uint4*>(q_s + (t * 8 + g) * q_bytes + ((s0 + k) * 4 + quad) * 16));
+        }
+      }
     }
 
     // key n is seen by query i when n <= len - nq + i: by query rows from H * (n - (len - nq)) on
