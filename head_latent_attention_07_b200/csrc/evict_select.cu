@@ -36,8 +36,11 @@ constexpr int kMaxCluster = 8;
 constexpr int kMaxStaged = 40960;      // keys of a CTA kept in shared memory (160 KB); later ones are read again
 
 struct SelectSmem {
-  uint32_t hist[2][kBins];                     // this CTA's counts; the rounds alternate
-  uint32_t coarse[kMaxCluster][kGroups];       // each CTA's counts in groups of 32 bins
+  // The rounds alternate between two copies of both counts.  What a CTA or its peers read of
+  // round r's copy after that round's cluster barrier is written again in round r + 2 at the
+  // earliest, behind the barrier of round r + 1, where every reader arrives after its reads.
+  uint32_t hist[2][kBins];                     // this CTA's counts
+  uint32_t coarse[2][kMaxCluster][kGroups];    // each CTA's counts in groups of 32 bins
   uint32_t kept[kMaxCluster], ties[kMaxCluster];
   uint32_t warp_a[32], warp_b[32];
   uint32_t found_bin, found_above, found_count;   // the bin of the wanted rank
@@ -155,6 +158,7 @@ evict_select_kernel(const SelectArgs a, const int cluster, const int staged_max)
     const int shift = round == 0 ? kFirstShift : max(0, 21 - __clz(hi - lo));   // (hi - lo) >> shift < kBins
     const uint32_t base = round == 0 ? kFirstLo : lo;
     uint32_t* hist = sm->hist[round & 1];
+    auto& coarse = sm->coarse[round & 1];
     auto count = [&](uint32_t k) {
       if (k >= lo && k <= hi) atomicAdd(&hist[k < base ? 0 : min((k - base) >> shift, kBins - 1u)], 1u);
     };
@@ -173,7 +177,7 @@ evict_select_kernel(const SelectArgs a, const int cluster, const int staged_max)
 #pragma unroll
     for (int j = 0; j < kGroups / (kMinThreads / 32); ++j) {
       const int g = warp + j * warps;
-      if (g < kGroups && lane < cluster) st_remote(mapa(smem_u32(&sm->coarse[rank][g]), lane), sum[j]);
+      if (g < kGroups && lane < cluster) st_remote(mapa(smem_u32(&coarse[rank][g]), lane), sum[j]);
     }
     sync();
     // the other counts were read before this barrier
@@ -183,8 +187,8 @@ evict_select_kernel(const SelectArgs a, const int cluster, const int staged_max)
       uint32_t c[2] = {0, 0}, v = 0, above, in_pair, in_group;
 #pragma unroll
       for (int r = 0; r < kMaxCluster; ++r) {
-        c[0] += r < cluster ? sm->coarse[r][kGroups - 1 - 2 * lane] : 0;
-        c[1] += r < cluster ? sm->coarse[r][kGroups - 2 - 2 * lane] : 0;
+        c[0] += r < cluster ? coarse[r][kGroups - 1 - 2 * lane] : 0;
+        c[1] += r < cluster ? coarse[r][kGroups - 2 - 2 * lane] : 0;
       }
       const int pair = lane_of_rank(c[0] + c[1], need, lane, &above);
       in_pair = __shfl_sync(0xffffffffu, c[0], pair);
