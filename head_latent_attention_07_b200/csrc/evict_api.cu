@@ -44,6 +44,33 @@ int device_sms(int* sms) {
   return cuda_status(cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev));
 }
 
+// Rows of `width` bytes, `stride` bytes apart, at p (null: not given).
+struct Buffer {
+  const void* p;
+  __int128 rows, width, stride;                  // a row stride may be as large as 64 bits hold
+};
+Buffer dense(const void* p, int64_t rows, int64_t width, int size) {
+  return {p, 1, (__int128)rows * width * size, (__int128)rows * width * size};
+}
+Buffer strided(const void* p, int64_t rows, int64_t width, int64_t stride, int size) {
+  return {p, rows, (__int128)width * size, (__int128)stride * size};
+}
+// The kernels read lengths, indices and masses more than once, in several CTAs: a buffer that
+// is written while others still read it would leave them with different sizes.  True when a
+// row of `out` shares a byte with one of the dense `others`; between its rows they may lie.
+template <int N>
+bool overlaps(const Buffer& out, const Buffer (&others)[N]) {
+  if (out.p == nullptr) return false;
+  const __int128 p = reinterpret_cast<uintptr_t>(out.p);
+  for (const Buffer& o : others) {
+    if (o.p == nullptr) continue;
+    const __int128 q = reinterpret_cast<uintptr_t>(o.p);
+    const __int128 row = q < p + out.width ? 0 : (q - p - out.width) / out.stride + 1;   // the first that ends behind q
+    if (row < out.rows && p + row * out.stride < q + o.width) return true;
+  }
+  return false;
+}
+
 // Spin budget of each bounded wait, as for the decode calls: kSpinLimitCycles, or the
 // environment variable MLA_SPIN_LIMIT (cycles, >= 0) when it is set.
 long long spin_limit_cycles() {
@@ -74,6 +101,12 @@ int mla_attn_mass(const mla_dims* dims, const mla_bf16* q_lat, const mla_bf16* p
   if (!aligned16(q_lat) || !aligned16(pool) || !aligned16(page_table) || !aligned16(seq_lens) || !aligned16(lse) ||
       !aligned16(mass) || (mass_lens && !aligned16(mass_lens)) || (dev_status && !aligned16(dev_status)))
     return MLA_ERR_MISALIGNED;
+  const int64_t rows = (int64_t)batch * nq * dims->n_heads, row = dims->d_c + dims->d_rope;
+  const int64_t tokens = (int64_t)max_pages * dims->page_size;
+  const Buffer read[] = {dense(q_lat, rows, row, 2), dense(pool, (int64_t)num_pages * dims->page_size, row, 2),
+                         dense(page_table, batch, max_pages, 4), dense(seq_lens, batch, 1, 4),
+                         dense(mass_lens, batch, 1, 4), dense(lse, rows, 1, 4)};
+  if (overlaps(strided(mass, batch, tokens, mass_stride, 4), read)) return MLA_ERR_INVALID_ARG;
   mla::MassArgs a;
   a.q_lat = q_lat; a.pool = pool; a.page_table = page_table; a.seq_lens = seq_lens; a.lse = lse;
   a.mass_lens = mass_lens; a.mass = mass; a.dev_status = dev_status; a.mass_stride = mass_stride;
@@ -97,6 +130,9 @@ int mla_evict_select(const float* mass, int64_t mass_stride, const int32_t* seq_
   if (!aligned16(mass) || !aligned16(seq_lens) || !aligned16(budgets) || !aligned16(keep_idx) ||
       !aligned16(new_lens) || (dev_status && !aligned16(dev_status)))
     return MLA_ERR_MISALIGNED;
+  const Buffer lens = dense(new_lens, batch, 1, 4), keep = dense(keep_idx, batch, keep_stride, 4);
+  const Buffer read[] = {dense(mass, batch, mass_stride, 4), dense(seq_lens, batch, 1, 4), dense(budgets, batch, 1, 4)};
+  if (overlaps(lens, {keep}) || overlaps(lens, read) || overlaps(keep, read)) return MLA_ERR_INVALID_ARG;
   int sms = 0, st = device_sms(&sms);
   if (st != MLA_OK) return st;
   mla::SelectArgs a;
@@ -120,6 +156,11 @@ int mla_cache_compact(const mla_dims* dims, mla_bf16* pool, const int32_t* page_
   if (!aligned16(pool) || !aligned16(page_table) || !aligned16(seq_lens) || !aligned16(keep_idx) ||
       !aligned16(new_lens) || (mass && !aligned16(mass)) || (dev_status && !aligned16(dev_status)))
     return MLA_ERR_MISALIGNED;
+  const Buffer rows = dense(pool, (int64_t)num_pages * dims->page_size, dims->d_c + dims->d_rope, 2);
+  const Buffer moved = strided(mass, batch, (int64_t)max_pages * dims->page_size, mass_stride, 4);
+  const Buffer read[] = {dense(page_table, batch, max_pages, 4), dense(seq_lens, batch, 1, 4),
+                         dense(keep_idx, batch, keep_stride, 4), dense(new_lens, batch, 1, 4)};
+  if (overlaps(moved, {rows}) || overlaps(moved, read) || overlaps(rows, read)) return MLA_ERR_INVALID_ARG;
   int sms = 0;
   if ((st = device_sms(&sms)) != MLA_OK) return st;
   mla::CompactArgs a;

@@ -361,7 +361,8 @@ int mla_query_proj(const mla_dims* dims, int32_t q_lora_rank, const mla_bf16* h,
  *   mass_lens  device int32 [batch]: leading tokens whose mass is meaningful, or NULL
  *              for seq_lens[b] - nq (mass was taken at the step before)
  *   mass       device fp32 [batch, mass_stride] (updated in place); row b starts
- *              at mass + b * mass_stride, mass_stride >= max_pages * page_size
+ *              at mass + b * mass_stride, mass_stride >= max_pages * page_size; must not
+ *              overlap an input (MLA_ERR_INVALID_ARG)
  *   dev_status device int32 word or NULL
  * Sums are fp32, in an order that does not depend on the schedule.  A sequence
  * whose length is out of range (see mla_decode_attn) and the tokens of a page
@@ -389,8 +390,10 @@ int mla_attn_mass(const mla_dims* dims, const mla_bf16* q_lat, const mla_bf16* p
  *   budgets    device int32 [batch], >= 0
  *   keep_idx   device int32 [batch, keep_stride] (output); row b starts at keep_idx +
  *              b * keep_stride, keep_stride >= min(L, budgets[b])
- *   new_lens   device int32 [batch] (output; must not overlap seq_lens or budgets)
+ *   new_lens   device int32 [batch] (output)
  *   dev_status device int32 word or NULL
+ * keep_idx and new_lens must overlap neither each other nor an input
+ * (MLA_ERR_INVALID_ARG): the lengths are read more than once while they are written.
  * A sequence whose length, budget or K is out of range records MLA_ERR_RANGE and
  * gets new_lens = 0.  batch <= 1024 and mass_stride <= 2^30 (else
  * MLA_ERR_UNSUPPORTED).
@@ -423,6 +426,7 @@ int mla_evict_select(const float* mass, int64_t mass_stride, const int32_t* seq_
  *   mass       device fp32 [batch, mass_stride] (updated in place) or NULL;
  *              mass_stride >= max_pages * page_size
  *   dev_status device int32 word or NULL
+ * pool and mass must overlap neither each other nor an input (MLA_ERR_INVALID_ARG).
  * Rows with keep_idx[b][j] == j are not touched.  An index outside [j, seq_lens[b])
  * or a page outside the pool records MLA_ERR_RANGE and row j stays as it was; a
  * sequence whose lengths are out of range records it and is left alone.
