@@ -23,6 +23,9 @@
 //               use): per group and tile 147 + 147 / 4 KB with the group resident, 147 + 147 /
 //               groups with the tile resident, so the tile is from more than 4 groups on.
 //
+// Page ids come by plain loads: this kernel may already be resident while the one before it on
+// the stream writes the table, so it is not read-only for the kernel's whole life.
+//
 // TMEM: two accumulators of NT columns, so that the sum over one tile runs beside the
 // next tile's MMAs.  Warps (256 threads): 0 loads (TMA), 1 owns TMEM and, in CTA 0, issues
 // the MMAs, 2 brings the groups' lse, 4-7 sum (warp w reads TMEM lanes 32 (w & 3) and
@@ -273,7 +276,7 @@ attn_mass_pair_kernel(const __grid_constant__ CUtensorMap tq, const __grid_const
     auto fetch = [&]() -> bool {
       if (!cur.next(&next)) return false;
       const int n = next.tile * kTileKeys + box_key;
-      if (has_box && n < next.len) next_id = __ldg(a.page_table + (size_t)next.b * a.max_pages + (n >> prm.page_shift));
+      if (has_box && n < next.len) next_id = a.page_table[(size_t)next.b * a.max_pages + (n >> prm.page_shift)];
       return true;
     };
     int s = 0, ri = -1;                          // the ring's stage, resident operands begun
@@ -397,7 +400,7 @@ attn_mass_pair_kernel(const __grid_constant__ CUtensorMap tq, const __grid_const
       if (!cur.next(&next)) return false;
       const int n = next.tile * kTileKeys + row;
       if (n < next.len) {
-        next_id = __ldg(a.page_table + (size_t)next.b * a.max_pages + (n >> prm.page_shift));
+        next_id = a.page_table[(size_t)next.b * a.max_pages + (n >> prm.page_shift)];
         if (next.group == 0 ? a.decay != 0.f : !kKeys) next_mass = a.mass[(size_t)next.b * a.mass_stride + n];
       }
       return true;

@@ -139,16 +139,18 @@ cache_compact_kernel(const __grid_constant__ CompactArgs a, const __grid_constan
   }
   const uint32_t ring0 = smem_u32(&sm->ring[0][tid]);
 
-  // the row that this thread looks up: row `row` of tile `kBatch * batch + tile`
+  // Indices and page ids by plain loads: this kernel may already be resident while the one before
+  // it writes them (the selection, keep_idx), so they are not read-only for its whole life.
+  // The row that this thread looks up: row `row` of tile `kBatch * batch + tile`
   const int tile = tid / kMaxTileRows, row = tid % kMaxTileRows;
   const int32_t* idx = a.keep_idx + (size_t)b * a.keep_stride;
   const int32_t* pages = a.page_table + (size_t)b * a.max_pages;
   auto position = [&](int r, int i) { return (r * cluster + rank) * rows + i; };
   auto index_of = [&](int batch) {             // j itself, which stays, where there is no such row
     const int j = position(batch * kBatch + tile, row);
-    return row < rows && j < new_len ? __ldg(idx + j) : j;
+    return row < rows && j < new_len ? idx[j] : j;
   };
-  auto page_of = [&](int n) { return __ldg(pages + (shift >= 0 ? n >> shift : n / a.page_size)); };
+  auto page_of = [&](int n) { return pages[shift >= 0 ? n >> shift : n / a.page_size]; };
   auto in_page = [&](int n) { return shift >= 0 ? n & (a.page_size - 1) : n % a.page_size; };
   int n_next = index_of(0);                    // the next batch's index, and what was found with the
   int j_now = 0, n_now = -1;                   // current one's: position, source index (-1: nothing

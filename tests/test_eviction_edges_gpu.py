@@ -5,7 +5,8 @@ import pytest
 import torch
 
 import head_latent_attention_07_b200 as M
-from mla_gpu_util import dev_i32
+import workload as W
+from mla_gpu_util import bits_of, dev_bf16, dev_i32
 from oracle import eviction as E
 from test_parity_eviction_gpu import masses
 
@@ -46,3 +47,45 @@ def test_select_beside_other_work(kind, batch, width):
         assert torch.equal(new[i], new[0]) and torch.equal(keep[i], keep[0]), f"call {i}"
     for b, w in enumerate(want):
         assert int(new[0][b]) == len(w) and np.array_equal(keep[0][b, : len(w)].cpu().numpy(), w), f"sequence {b}"
+
+
+@pytest.mark.parametrize("replays", [0, 3])
+def test_choices_rewritten_before_each_compaction(replays):
+    """Choice after choice into the same buffers, each compacted right behind its selection, whose
+    kernel is still at work when the compaction's starts: it must see the new indices and lengths,
+    not those of the round before, eager and from a replayed graph."""
+    lens, rounds = [900, 64, 3000, 1], 12
+    g = np.random.default_rng(41)
+    m = np.exp(g.standard_normal((rounds, 4, 3072))).astype(np.float32)
+    budgets = [np.minimum(lens, [300 + 17 * i, 1 + 5 * i, 2900 - 211 * i, 1]) for i in range(rounds)]
+    table, pages = W.make_page_table(np.asarray(lens, dtype=np.int32), 64, 5, True, 2)
+    bits = W.bf16_bits(g.standard_normal((pages, 64, 80), dtype=np.float32))
+    dims = M.MlaDims(n_heads=1, d_c=64, d_rope=16, qk_nope=32, v_head=64, d_model=64, page_size=64)
+    pools = [dev_bf16(bits) for _ in range(rounds)]
+    mass, room = [torch.from_numpy(x).cuda() for x in m], [dev_i32(x) for x in budgets]
+    page_table, seq_lens = dev_i32(table), dev_i32(lens)
+    keep = torch.full((4, 3000), -1, dtype=torch.int32, device="cuda")
+    new = torch.zeros(4, dtype=torch.int32, device="cuda")
+    status = torch.zeros(4, dtype=torch.int32, device="cuda")
+
+    def calls():
+        for i in range(rounds):
+            M.mla_evict_select(mass[i], seq_lens, room[i], keep, new, n_sink=2, n_recent=3, dev_status=status)
+            M.mla_cache_compact(dims, pools[i], page_table, seq_lens, keep, new, rerotate=False, dev_status=status)
+
+    if replays == 0:
+        calls()
+    else:
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            calls()
+    for _ in range(replays):
+        for pool in pools:
+            pool.copy_(dev_bf16(bits))
+        graph.replay()
+    torch.cuda.synchronize()
+    assert M.mla_status_read(status) == 0
+    for i in range(rounds):
+        want, _ = E.compact(W.bf16_to_f32(bits), table, E.select(m[i], lens, budgets[i], 2, 3), 64, rerotate=False)
+        assert np.array_equal(bits_of(pools[i]), W.bf16_bits(want.astype(np.float32))), f"round {i}"
