@@ -104,15 +104,7 @@ attn_mass_kernel(const MassArgs a) {
     for (int c = warp; c < tiles * 8; c += kThreads / 32)
       for (int v = lane; v < per_row; v += 32)
         cp_async16_or_zero(q_dst + c * q_bytes + v * 16, qb + (size_t)c * R + v * 8, qb, c < cols && v < rv);
-    if (threadIdx.x < kCols) {
-      // a row that saw no key (lse = -inf) gives nothing: exp2(x - inf) = 0
-      float l = INFINITY;
-      if ((int)threadIdx.x < cols) {
-        l = a.lse[(size_t)b * rows_total + c0 + threadIdx.x];
-        l = l == -INFINITY ? INFINITY : l * kLog2e;
-      }
-      lse2[threadIdx.x] = l;
-    }
+    if ((int)threadIdx.x < cols) lse2[threadIdx.x] = a.lse[(size_t)b * rows_total + c0 + threadIdx.x] * kLog2e;
     asm volatile("cp.async.wait_all;" ::: "memory");
     __syncthreads();
 
@@ -135,7 +127,8 @@ attn_mass_kernel(const MassArgs a) {
       }
     }
 
-    // key n is seen by query i when n <= len - nq + i: by query rows from H * (n - (len - nq)) on
+    // key n is seen by query i when n <= len - nq + i: by query rows from H * (n - (len - nq)) on.
+    // A row that saw no key (lse = -inf) gives nothing, whatever its query holds.
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       const int first = max(0, n[j] - (len - a.nq)) * a.n_heads - c0;
@@ -144,7 +137,8 @@ attn_mass_kernel(const MassArgs a) {
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
           const int col = t * 8 + quad * 2 + k;
-          if (col < cols && col >= first) w[j] += sm100::ex2(fmaf(acc[t][j * 2 + k], sl2, -lse2[col]));
+          if (col < cols && col >= first && lse2[col] != -INFINITY)
+            w[j] += sm100::ex2(fmaf(acc[t][j * 2 + k], sl2, -lse2[col]));
         }
     }
   }

@@ -84,6 +84,7 @@ struct Bars {
   uint64_t drain;        // both: every MMA issued has completed
   uint32_t tmem_base;
   int abort;
+  int keyless;           // beside the lse: some row of the group saw no key (lse = -inf)
 };
 static_assert(Layout<256, false>::kOffBar + sizeof(Bars) <= Layout<256, false>::kOffRes, "barrier area");
 
@@ -372,15 +373,17 @@ attn_mass_pair_kernel(const __grid_constant__ CUtensorMap tq, const __grid_const
       const int cols = prm.rows_total - it.group * NT;
       const float* src = a.lse + (size_t)it.b * prm.rows_total + it.group * NT;
       float l[NT / 32];
+      bool keyless = false;
 #pragma unroll
       for (int i = 0; i < NT / 32; ++i) {
-        // a row that saw no key (lse = -inf) gives nothing: exp2(x - inf) = 0
-        l[i] = i * 32 + lane < cols ? src[i * 32 + lane] : INFINITY;
-        l[i] = l[i] == -INFINITY ? INFINITY : l[i] * 1.4426950408889634f;
+        l[i] = (i * 32 + lane < cols ? src[i * 32 + lane] : 0.f) * 1.4426950408889634f;
+        keyless |= l[i] == -INFINITY;
       }
+      keyless = __any_sync(0xffffffffu, keyless);
       if (gi > 0 && !wwait(&bar->lse_empty, (gi - 1) & 1)) break;
 #pragma unroll
       for (int i = 0; i < NT / 32; ++i) lse2[i * 32 + lane] = l[i];
+      if (lane == 0) bar->keyless = keyless;
       __syncwarp();
       if (lane == 0) mbar_arrive(&bar->lse_full);
       ++gi;
@@ -406,6 +409,7 @@ attn_mass_pair_kernel(const __grid_constant__ CUtensorMap tq, const __grid_const
       return true;
     };
     int t = 0, gi = -1;
+    bool keyless = false;
     float sum_so_far = 0.f;                      // what the key has collected
     bool more = fetch();
     while (more) {
@@ -423,13 +427,16 @@ attn_mass_pair_kernel(const __grid_constant__ CUtensorMap tq, const __grid_const
       if (kKeys || it.first) {
         ++gi;
         if (!wwait(&bar->lse_full, gi & 1)) break;
+        keyless = *static_cast<volatile int*>(&bar->keyless) != 0;
       }
       if (!wwait(&bar->acc_full[t & 1], (t >> 1) & 1)) break;
       tc_fence_after();
       const uint32_t acc = lanes + (t & 1) * NT;
       // key n is seen by query i when n <= len - nq + i: by query rows from H * (n - (len - nq)) on
       const int first = max(0, n - (it.len - a.nq)) * a.n_heads - it.group * NT;
-      const bool all = __all_sync(0xffffffffu, first <= 0);
+      // A row that saw no key gives nothing, whatever its query holds (padding: NaN too), so it is
+      // left out and not multiplied away; groups with such a row take the branch that looks.
+      const bool all = __all_sync(0xffffffffu, first <= 0) && !keyless;
       float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 1
       for (int c0 = 0; c0 < cols; c0 += 32) {
@@ -448,8 +455,8 @@ attn_mass_pair_kernel(const __grid_constant__ CUtensorMap tq, const __grid_const
         } else {
 #pragma unroll
           for (int i = 0; i < 32; ++i) {
-            const float e = ex2(fmaf(v[i], prm.scale_log2, -lse2[c0 + i]));
-            if (c0 + i >= first && c0 + i < cols) sum[i & 3] += e;
+            const float l = lse2[c0 + i], e = ex2(fmaf(v[i], prm.scale_log2, -l));
+            if (c0 + i >= first && c0 + i < cols && l != -INFINITY) sum[i & 3] += e;
           }
         }
       }

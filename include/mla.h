@@ -355,7 +355,8 @@ int mla_query_proj(const mla_dims* dims, int32_t q_lora_rank, const mla_bf16* h,
  *              those of the last nq tokens of a chunk: an observation window)
  *   pool, page_table, seq_lens   as for mla_decode_attn
  *   lse        device fp32 [batch, nq, H], as returned by mla_decode_attn for these
- *              queries; a row with lse = -inf (it saw no key) gives nothing
+ *              queries; a row with lse = -inf (it saw no key, or is padding) gives
+ *              nothing, whatever its query holds
  *   decay      0..1: 1 accumulates, less lets old mass fade, 0 starts anew (old
  *              mass is then not read)
  *   mass_lens  device int32 [batch]: leading tokens whose mass is meaningful, or NULL

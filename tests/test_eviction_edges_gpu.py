@@ -8,7 +8,7 @@ import head_latent_attention_07_b200 as M
 import workload as W
 from mla_gpu_util import bits_of, dev_bf16, dev_i32
 from oracle import eviction as E
-from test_parity_eviction_gpu import masses
+from test_parity_eviction_gpu import Cache, masses
 
 pytestmark = pytest.mark.gpu
 
@@ -89,3 +89,34 @@ def test_choices_rewritten_before_each_compaction(replays):
     for i in range(rounds):
         want, _ = E.compact(W.bf16_to_f32(bits), table, E.select(m[i], lens, budgets[i], 2, 3), 64, rerotate=False)
         assert np.array_equal(bits_of(pools[i]), W.bf16_bits(want.astype(np.float32))), f"round {i}"
+
+
+# ------------------------------------------------------------------ attention mass
+
+@pytest.mark.parametrize("shape", [dict(), dict(d_c=64, d_rope=16, nope=32), dict(d_c=64, d_rope=16, nope=32, page=48)])
+@pytest.mark.parametrize("nq,heads", [(1, 8), (2, 40), (2, 128), (4, 128), (11, 128)])
+def test_mass_of_padded_queries(nq, heads, shape):
+    """Rows with lse = -inf give nothing even where their query is NaN or infinite (slots of a
+    batch that hold no query): the bits are those of the same call with ordinary queries there,
+    and without such rows nothing changes."""
+    lens = [700, 70, 300]
+    c = Cache(lens, nq, heads, seed=nq + heads, **shape).make_lse()
+    plain = c.run()
+    c.lse_host[0, nq // 2, 1 : heads - 1 : 3] = -np.inf
+    c.lse_host[1] = -np.inf
+    c.lse_host[2, nq - 1, 0] = -np.inf
+    c.lse = torch.from_numpy(c.lse_host).cuda()
+    none = np.isinf(c.lse_host)
+    restart = lambda: setattr(c, "mass", torch.from_numpy(c.mass0).cuda())
+    restart()
+    want = c.run()
+    rows = np.abs(want - c.want())
+    for b, n in enumerate(lens):
+        assert (rows[b, :n] <= c.tolerance() * np.abs(c.want()[b, :n])).all()
+    assert not np.array_equal(want, plain)
+    for bits in (0x7FC0, 0x7F80, 0xFF80, 0x7F7F):          # NaN, both infinities, the largest number
+        c.q_bits[none] = bits
+        c.q = dev_bf16(c.q_bits)
+        restart()
+        assert np.array_equal(c.run(), want), hex(bits)
+    assert M.mla_status_read(c.status) == 0
