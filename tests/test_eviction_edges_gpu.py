@@ -8,7 +8,7 @@ import head_latent_attention_07_b200 as M
 import workload as W
 from mla_gpu_util import bits_of, dev_bf16, dev_i32
 from oracle import eviction as E
-from test_parity_eviction_gpu import Cache, masses
+from test_parity_eviction_gpu import Cache, check_compact, check_select, choose, masses
 
 pytestmark = pytest.mark.gpu
 
@@ -120,3 +120,97 @@ def test_mass_of_padded_queries(nq, heads, shape):
         restart()
         assert np.array_equal(c.run(), want), hex(bits)
     assert M.mla_status_read(c.status) == 0
+
+
+class LongCache:
+    """A cache of many tiles (more than five for each CTA pair of the GPU, in ragged sequences, so
+    that shares begin and end inside them), its queries and its mass in 64 bits, all on the GPU."""
+
+    LENS = [33001, 9, 1300, 256, 20011, 257, 700, 25600, 255, 17500, 15003]     # 450 tiles of 256 tokens
+
+    def __init__(self, nq, heads, d_c, d_rope, page, decay):
+        g = torch.Generator(device="cuda").manual_seed(1000 * nq + heads + d_c)
+        self.lens, self.nq, self.decay = [max(n, nq) for n in self.LENS], nq, decay
+        row, B = d_c + d_rope, len(self.lens)
+        table, pages = W.make_page_table(np.asarray(self.lens, dtype=np.int32), page, 3, True, 2)
+        self.dims = M.MlaDims(n_heads=heads, d_c=d_c, d_rope=d_rope, qk_nope=128, v_head=64, d_model=64, page_size=page)
+        self.pool = torch.randn(pages, page, row, generator=g, device="cuda").bfloat16()
+        self.q = (0.5 * torch.randn(B, nq, heads, row, generator=g, device="cuda")).bfloat16()
+        self.page_table, self.seq_lens = dev_i32(table), dev_i32(self.lens)
+        self.mass0 = torch.exp(torch.randn(B, table.shape[1] * page, generator=g, device="cuda"))
+        self.lse = torch.empty(B, nq, heads, device="cuda")
+        self.status = torch.zeros(4, dtype=torch.int32, device="cuda")
+        scale = 1.0 / np.sqrt(128 + d_rope)
+        self.want, largest = self.mass0.double(), 0.0
+        for b, n in enumerate(self.lens):
+            keys = self.pool[self.page_table[b, : -(-n // page)].long()].view(-1, row)[:n].double()
+            q = self.q[b].double().view(nq * heads, row)
+            s = (q @ keys.T).mul_(scale).view(nq, heads, n)
+            seen = torch.arange(n, device="cuda")[None, :] <= (n - nq + torch.arange(nq, device="cuda"))[:, None]
+            s.masked_fill_(~seen[:, None, :], -float("inf"))
+            self.lse[b] = torch.logsumexp(s, 2).float()
+            w = torch.exp(s.sub_(self.lse[b].double()[..., None])).sum(dim=(0, 1))
+            w[: n - nq] += decay * self.mass0[b, : n - nq].double()
+            self.want[b, :n] = w
+            largest = max(largest, float((q.float().abs() @ keys.float().abs().T).max()))
+        # the product's, the exponent's and the sum's errors as the parity tests derive them; the old
+        # mass is rounded once with its decay and once in the sum
+        self.tol = (scale * 1.001 * largest * (row / 16 + 16) * 2**-23 + 2 * float(self.lse.abs().max()) * 1.4427 * 2**-23
+                    + 2**-22 + nq * heads * 2**-24 + 2**-23)
+
+    def run(self, only=slice(None)):
+        mass = self.mass0[only].clone()
+        M.mla_attn_mass(self.dims, self.q[only], self.pool, self.page_table[only].clone(), self.seq_lens[only].clone(),
+                        self.lse[only].clone(), mass, decay=self.decay, dev_status=self.status)
+        torch.cuda.synchronize()
+        return mass
+
+
+@pytest.mark.parametrize("decay", [0.5, 0.0])
+@pytest.mark.parametrize("nq,heads,d_c,d_rope,page", [
+    (1, 128, 512, 64, 64),     # 128 query rows, resident; the ring laps, both accumulators are used again
+    (1, 5, 512, 64, 256),
+    (2, 128, 512, 64, 64),     # 256 rows: one group
+    (3, 128, 512, 64, 64),     # two and four groups over tiles in fours; the sums pass through the mass
+    (8, 128, 512, 64, 32),
+    (9, 128, 512, 64, 64),     # five groups: the keys resident, tile after tile
+    (1, 16, 64, 16, 64),       # narrow rows
+    (3, 128, 64, 16, 8),
+    (9, 128, 64, 16, 128),
+])
+def test_mass_many_tiles_per_pair(nq, heads, d_c, d_rope, page, decay):
+    c = LongCache(nq, heads, d_c, d_rope, page, decay)
+    got = c.run()
+    assert M.mla_status_read(c.status) == 0
+    for b, n in enumerate(c.lens):
+        off = ((got[b, :n].double() - c.want[b, :n]).abs() / c.want[b, :n]).max()
+        assert float(off) <= c.tol, f"sequence {b}: off by {float(off):.2e} (<= {c.tol:.2e})"
+        assert torch.equal(got[b, n:], c.mass0[b, n:]), "mass past the end changed"
+    # the same bits from one sequence alone, whose tiles are shared out otherwise
+    for b in (0, 4, 10):
+        assert torch.equal(c.run(slice(b, b + 1))[0], got[b])
+    # tokens of a page outside the pool keep their mass, all others theirs
+    c.page_table[0, 2:6] = 2**31 - 1
+    again = c.run()
+    assert M.mla_status_read(c.status) == M.MLA_ERR_RANGE
+    assert torch.equal(again[0, 2 * page : 6 * page], c.mass0[0, 2 * page : 6 * page])
+    again[0, 2 * page : 6 * page] = got[0, 2 * page : 6 * page]
+    assert torch.equal(again, got)
+
+
+# ------------------------------------------------------------------ compaction
+
+@pytest.mark.parametrize("batch", [1, 5, 10, 19, 38, 75])
+@pytest.mark.parametrize("rerotate", [True, False])
+def test_compact_short_sequences_in_wide_tables(batch, rerotate):
+    """A page table and mass rows as wide as the longest context of an engine over sequences far
+    shorter, at batches between the powers of two: launch shapes come from the width."""
+    lens = [1 + (1237 * b + 700) % 2500 for b in range(batch)]
+    c = Cache(lens, 1, 1, 64, 16, seed=batch, max_pages=131072 // 64)
+    check_compact(c, choose(lens, 0.6, batch, sink=2), rerotate=rerotate)
+
+
+@pytest.mark.parametrize("batch", [1, 5, 10, 19, 38, 75])
+def test_select_short_sequences_in_wide_rows(batch):
+    lens = [1 + (1237 * b + 700) % 2500 for b in range(batch)]
+    check_select(masses("spread", (batch, 131072), batch), lens, np.maximum(1, np.array(lens) // 3), 2, 40)
