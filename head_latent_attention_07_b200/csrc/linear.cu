@@ -106,7 +106,7 @@ __global__ void __launch_bounds__(kLinThreads, 4) token_linear_kernel(const Line
   // own wait, so everything earlier on the stream has completed).
   load_w(s_lo + warp);
   if (SPLIT) cluster_arrive_relaxed();  // paired with the wait before the first remote store
-  grid_dependency_wait();  // x is written by the preceding kernel
+  grid_dependency_wait();  // x is written by the preceding kernel (so plain loads, not read-only ones)
   allow_dependent_launch();
 
   for (int s0 = s_lo + warp; s0 < s_hi; s0 += kLinWarps * U) {
@@ -118,7 +118,7 @@ __global__ void __launch_bounds__(kLinThreads, 4) token_linear_kernel(const Line
       const bool k_ok = s < s_hi && k + 8 * q < K;
 #pragma unroll
       for (int j = 0; j < NT; ++j)
-        b[u][j] = (k_ok && x_ok[j]) ? __ldg(reinterpret_cast<const uint4*>(xr[j] + k)) : zero;
+        b[u][j] = (k_ok && x_ok[j]) ? *reinterpret_cast<const uint4*>(xr[j] + k) : zero;
     }
 #pragma unroll
     for (int u = 0; u < U; ++u)
