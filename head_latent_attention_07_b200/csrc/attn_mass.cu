@@ -15,7 +15,7 @@
 // of their products, and are read again from L2 for every block.
 //
 // Latency binds it, of the keys' loads and of the staging, at 16 warps per SM: 16 x 32768
-// tokens 640 wide take 490 us at 128 heads (175 TFLOP/s) and 173 us at 16 (3.9 TB/s).  With
+// tokens 640 wide take 497 us at 128 heads (173 TFLOP/s) and 174 us at 16 (3.9 TB/s).  With
 // each slice loaded when it was needed it was 848 and 260 us, with the query rows staged
 // through registers 551 and 181.  It is for the shapes that the CTA-pair kernel does not
 // take: rows over 576, other page sizes.
@@ -31,7 +31,7 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kKeys = 128;       // keys per CTA, 16 per warp
 constexpr int kCols = 64;        // query rows per block
-constexpr int kAhead = 2;        // 32-column slices of the keys on their way (4 spill registers)
+constexpr int kAhead = 2;        // 32-column slices of the keys on their way (114 registers, no spills; 4 spilled)
 constexpr float kLog2e = 1.4426950408889634f;
 
 // Bytes of one staged query row: whole 32-column slices, and 64 bytes modulo 128,
@@ -104,9 +104,14 @@ attn_mass_kernel(const MassArgs a) {
     for (int c = warp; c < tiles * 8; c += kThreads / 32)
       for (int v = lane; v < per_row; v += 32)
         cp_async16_or_zero(q_dst + c * q_bytes + v * 16, qb + (size_t)c * R + v * 8, qb, c < cols && v < rv);
-    if ((int)threadIdx.x < cols) lse2[threadIdx.x] = a.lse[(size_t)b * rows_total + c0 + threadIdx.x] * kLog2e;
+    bool keyless = false;                                  // lse = -inf: the row saw no key
+    if ((int)threadIdx.x < cols) {
+      const float l = a.lse[(size_t)b * rows_total + c0 + threadIdx.x] * kLog2e;
+      lse2[threadIdx.x] = l;
+      keyless = l == -INFINITY;
+    }
     asm volatile("cp.async.wait_all;" ::: "memory");
-    __syncthreads();
+    const bool some_keyless = __syncthreads_or(keyless);
 
     float acc[8][4];
 #pragma unroll
@@ -128,19 +133,24 @@ attn_mass_kernel(const MassArgs a) {
     }
 
     // key n is seen by query i when n <= len - nq + i: by query rows from H * (n - (len - nq)) on.
-    // A row that saw no key (lse = -inf) gives nothing, whatever its query holds.
+    // A row that saw no key gives nothing, whatever its query holds; a block of queries without
+    // such a row does not look for them (looking in every block: 524 us against 497).
+    auto add = [&](auto look) {
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int first = max(0, n[j] - (len - a.nq)) * a.n_heads - c0;
+      for (int j = 0; j < 2; ++j) {
+        const int first = max(0, n[j] - (len - a.nq)) * a.n_heads - c0;
 #pragma unroll
-      for (int t = 0; t < 8; ++t)
+        for (int t = 0; t < 8; ++t)
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const int col = t * 8 + quad * 2 + k;
-          if (col < cols && col >= first && lse2[col] != -INFINITY)
-            w[j] += sm100::ex2(fmaf(acc[t][j * 2 + k], sl2, -lse2[col]));
-        }
-    }
+          for (int k = 0; k < 2; ++k) {
+            const int col = t * 8 + quad * 2 + k;
+            if (col < cols && col >= first && (!look() || lse2[col] != -INFINITY))
+              w[j] += sm100::ex2(fmaf(acc[t][j * 2 + k], sl2, -lse2[col]));
+          }
+      }
+    };
+    if (some_keyless) add([] { return true; });
+    else add([] { return false; });
   }
 
 #pragma unroll
