@@ -32,9 +32,10 @@
 // on).  Every mbarrier wait is bounded: on time-out the kernel records MLA_ERR_TIMEOUT,
 // drains its MMAs and ends.
 //
-// Measured, 128 heads, R = 576, bursts: 16 x 32768 103 us (5.9 TB/s, 0.90 of a copy); 64
-// ragged, 2 tokens each 556 us (4.8 TB/s and 1.22 PFLOP/s: both pipes, at 1.4 GHz); 2 x 32768,
-// 32 tokens each 210 us (1.47 PFLOP/s).  Long loops run under the power cap, up to 13 % slower.
+// Measured, 128 heads, R = 576, a dozen calls back to back in a graph: 16 x 32768 102 us (6.0
+// TB/s, 0.91 of a copy); 64 ragged, 2 tokens each 555 us (4.5 TB/s and 1.13 PFLOP/s: both
+// pipes, at 1.4 GHz); 2 x 32768, 32 tokens each 210 to 219 us (1.41 to 1.47 PFLOP/s).  Loops of
+// calls from Python run under the power cap: 112 to 120, 570 to 615 and 240 to 246 us, by the box.
 #include <cuda.h>
 
 #include "common.cuh"

@@ -24,7 +24,7 @@
 // every kBatch tiles, and its three dependent loads are a batch apart.  (One bulk copy per
 // row, by one thread, was bound by its issue, 40 ns each; roles in warps of their own,
 // by the six hand-overs of a tile.)  Measured: 16 x 32768, half kept, 110 us, 5.5 TB/s of read
-// and written rows, 0.83 of a copy.
+// and written rows, 0.83 of a copy; without turning 111, and 106 without a mass either.
 #include "common.cuh"
 #include "evict.h"
 #include "sm100.cuh"
@@ -57,8 +57,11 @@ __device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_gr
 // rotation per position as a fraction of a full turn.  delta * turn modulo 2^64 is the
 // whole rotation modulo one turn, exactly, so far moves keep their phase.  Its upper 23
 // bits, rounded, become a float in [-1/2, 1/2) by their position in it (a conversion would go
-// to the unit of the sine and cosine, which is the busy one): an angle good to 2^-21.3 and
-// the hardware's sine and cosine, good to 2^-21.4, against the 2^-9 of the bf16 result.
+// to the unit of the sine and cosine, which is the busy one).  At worst: the angle is off by
+// 2 pi 2^-24 from those bits, 2^-23 from the product's rounding and 2^-23.4 from the constant's,
+// 2^-20.7 together; the hardware's sine by 2^-21.41 and its cosine by 2^-21.19 on [-pi, pi] (the
+// bounds that CUDA documents), 2^-20.8 of the pair's length in one coordinate; the three
+// fp32 roundings by 2^-23.  All of it, 2^-19.6 of the length, against the 2^-8 of a bf16 result.
 __device__ __forceinline__ uint32_t turn_pair(uint32_t xy, int delta, uint64_t turn) {
   const uint32_t phase = (uint32_t)(((uint64_t)(int64_t)delta * turn) >> 32);
   const float ang = (__uint_as_float(0x3F800000u | ((phase + 0x80000100u) >> 9)) - 1.5f) * 6.283185307f;
@@ -80,7 +83,8 @@ constexpr uint32_t kNone = 0xFFFFFFFFu;
 struct CompactSmem {
   uint4 ring[kStages][kThreads * kPieces];
   // the rows of a tile, by batch: pool rows (kNone: the row stays) and the distance
-  // moved (0: neither row nor mass moves)
+  // moved (0: neither row nor mass moves; the mass lies in no page, so it moves beside a row
+  // that stays because a page of it is outside the pool)
   uint32_t src[2][kThreads];
   uint32_t dst[3][kThreads];
   int delta[3][kThreads];
@@ -275,6 +279,10 @@ cudaError_t launch_cache_compact(const CompactArgs& a, int sms, cudaStream_t str
   //    8 x 32768           4 x 4   72   8 x 2   62   8 x 4   68
   //    4 x 32768           4 x 4   56   8 x 4   44   8 x 8   32
   //    8 x 4096            8 x 2   16   8 x 4   11
+  // (64 x 8192 would be 4 % better off with 2 x 1.)  Both numbers only double, so a batch just past
+  // a step fills about half of the SMs: 5 x 32768 63 us (2.9 TB/s, against 4.6 at 4 and at 8), 10 x
+  // 32768 106 (3.5), 19 x 32768 204 (3.5), 38 x 27584 346 (3.5), 75 x 13952 331 (3.6; 5.9 at 74).
+  // "Short" goes by the table's width: 8 x 4096 under a table for 131072 tokens 10.7 us (10.1).
   const int64_t tiles = ((int64_t)a.max_pages * a.page_size + kMaxTileRows - 1) / kMaxTileRows;
   geo.slices = 1;
   while (geo.slices < kMaxSlices && geo.slices * 16 <= plain && (int64_t)4 * geo.slices * a.batch <= sms) geo.slices *= 2;

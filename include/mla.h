@@ -367,7 +367,11 @@ int mla_query_proj(const mla_dims* dims, int32_t q_lora_rank, const mla_bf16* h,
  *   dev_status device int32 word or NULL
  * Sums are fp32, in an order that does not depend on the schedule.  A sequence
  * whose length is out of range (see mla_decode_attn) and the tokens of a page
- * outside the pool keep their mass; both record MLA_ERR_RANGE.  batch and nq as
+ * outside the pool keep their mass; both record MLA_ERR_RANGE.  After MLA_ERR_TIMEOUT
+ * the mass of every sequence of the call is undefined (some tokens already hold the
+ * step's share, some only a part of it): restore it, or start anew with decay = 0 or
+ * mass_lens = 0, before it is used.  The whole cache of a sequence has to be in this
+ * pool: there is no form for one rank's window of a context split.  batch and nq as
  * for mla_decode_attn, max_pages * page_size <= 2^30 (else MLA_ERR_UNSUPPORTED).
  * Rows up to 576 wide in pages of 8 to 256 tokens, a power of two, run on the
  * tensor cores' pair instructions; other shapes on a slower kernel.
@@ -429,8 +433,12 @@ int mla_evict_select(const float* mass, int64_t mass_stride, const int32_t* seq_
  *   dev_status device int32 word or NULL
  * pool and mass must overlap neither each other nor an input (MLA_ERR_INVALID_ARG).
  * Rows with keep_idx[b][j] == j are not touched.  An index outside [j, seq_lens[b])
- * or a page outside the pool records MLA_ERR_RANGE and row j stays as it was; a
- * sequence whose lengths are out of range records it and is left alone.
+ * records MLA_ERR_RANGE and leaves row j and its mass as they were.  A page outside the
+ * pool, of n or of j, records it and leaves row j as it was; the mass, which lies in no
+ * page, becomes that of n all the same, so row and mass of such a j no longer belong
+ * together.  A sequence whose lengths are out of range records it and is left alone.
+ * The angle of a turn is exact modulo a full turn; it, its sine and its cosine are taken
+ * in fp32, off by at most 2^-19.6 of the pair's length together, before the rounding to bf16.
  * batch <= 1024, max_pages * page_size <= 2^30 and num_pages * page_size <
  * 2^32 - 1 (else MLA_ERR_UNSUPPORTED).
  */
