@@ -89,10 +89,9 @@ cudaError_t launch_decode_combine(const DecodeArgs& a, cudaStream_t stream);
 // LSE merge of the ranks' partials, then W_UV: a.batch = tokens, a.nq = 1.
 cudaError_t launch_merge_ranks(const DecodeArgs& a, const RankSources& src, cudaStream_t stream);
 
-// 2-D TMA map over bf16 rows of 576 elements (row stride 1152 bytes) with a box
-// of [box_rows x box_cols] elements (tma_map.cu).
-bool encode_rows576(CUtensorMap* m, const void* base, uint64_t rows, uint32_t box_cols, uint32_t box_rows,
-                    CUtensorMapSwizzle sw);
+// 2-D TMA map over dense bf16 rows of `width` elements with a box of [box_rows x 64]
+// elements, 128-byte swizzle; what lies outside reads as zero (tma_map.cu).
+bool encode_rows(CUtensorMap* m, const void* base, uint64_t rows, uint32_t width, uint32_t box_rows);
 
 // Tensor-core split kernel on CTA pairs (d_c = 512, d_rope = 64, 64-token pages).
 bool decode_pair_supported(int d_c, int d_rope, int page_size);

@@ -722,8 +722,7 @@ cudaError_t launch_decode_split_pair(const DecodeArgs& a, long long spin_limit, 
   CUtensorMap tq, tp;
   const uint64_t qrows = (uint64_t)a.batch * rows_total;
   const uint64_t prows = (uint64_t)a.num_pages * 64;
-  if (!encode_rows576(&tq, a.q_lat, qrows, 64, 64, CU_TENSOR_MAP_SWIZZLE_128B) ||
-      !encode_rows576(&tp, a.pool, prows, 64, 64, CU_TENSOR_MAP_SWIZZLE_128B))
+  if (!encode_rows(&tq, a.q_lat, qrows, 576, 64) || !encode_rows(&tp, a.pool, prows, 576, 64))
     return cudaErrorInvalidValue;
   PairParams prm;
   prm.d = a;

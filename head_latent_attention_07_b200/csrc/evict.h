@@ -48,8 +48,6 @@ struct CompactArgs {
   uint64_t turn[kMaxRopePairs];  // theta^(-2i/d_rope) / (2 pi) of pair i, as a fraction of a turn times 2^64
 };
 
-bool encode_rows(CUtensorMap* m, const void* base, uint64_t rows, uint32_t width, uint32_t box_rows);
-
 // Tensor-core pairs (rows up to 576 wide, pages of a power of two), and any other shape.
 bool attn_mass_pair_supported(const MassArgs& a);
 cudaError_t launch_attn_mass_pair(const MassArgs& a, int sms, long long spin_limit, cudaStream_t stream);

@@ -1,4 +1,4 @@
-// Tensor maps (TMA descriptors) over the 576-wide latent rows.
+// Tensor maps (TMA descriptors) over the latent rows of queries and cache.
 #include <cuda.h>
 
 #include <mutex>
@@ -28,17 +28,15 @@ EncodeTiledFn encode_fn() {
 
 }  // namespace
 
-// 2-D bf16 map over [rows, 576] with row stride 1152 bytes, box [box_rows, box_cols].
-bool encode_rows576(CUtensorMap* m, const void* base, uint64_t rows, uint32_t box_cols, uint32_t box_rows,
-                    CUtensorMapSwizzle sw) {
+bool encode_rows(CUtensorMap* m, const void* base, uint64_t rows, uint32_t width, uint32_t box_rows) {
   EncodeTiledFn fn = encode_fn();
   if (fn == nullptr) return false;
-  cuuint64_t dims[2] = {576, rows};
-  cuuint64_t strides[1] = {576 * 2};
-  cuuint32_t box[2] = {box_cols, box_rows};
+  cuuint64_t dims[2] = {width, rows};
+  cuuint64_t strides[1] = {width * 2};
+  cuuint32_t box[2] = {64, box_rows};
   cuuint32_t es[2] = {1, 1};
   return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, es,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, sw, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
