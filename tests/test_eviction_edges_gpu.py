@@ -1,5 +1,7 @@
 """The eviction calls where their parts have to wait for one another, and at the edges of
 what their contract allows."""
+from concurrent.futures import ThreadPoolExecutor
+
 import numpy as np
 import pytest
 import torch
@@ -8,6 +10,7 @@ import head_latent_attention_07_b200 as M
 import workload as W
 from mla_gpu_util import bits_of, dev_bf16, dev_i32
 from oracle import eviction as E
+from test_eviction_use_gpu import Loop, same
 from test_parity_eviction_gpu import Cache, check_compact, check_select, choose, masses
 
 pytestmark = pytest.mark.gpu
@@ -214,3 +217,26 @@ def test_compact_short_sequences_in_wide_tables(batch, rerotate):
 def test_select_short_sequences_in_wide_rows(batch):
     lens = [1 + (1237 * b + 700) % 2500 for b in range(batch)]
     check_select(masses("spread", (batch, 131072), batch), lens, np.maximum(1, np.array(lens) // 3), 2, 40)
+
+
+# ------------------------------------------------------------------ together
+
+def test_calls_from_several_threads():
+    """Loops of other sizes issued by host threads of their own, each on a stream of its own."""
+    shapes = [dict(nq=2, heads=128), dict(nq=1, heads=40), dict(nq=9, heads=64),
+              dict(nq=1, heads=4, page=48, d_c=64, d_rope=16)]
+    lens = [[3000, 2000], [700, 64, 1500], [9, 900], [2500, 300, 77, 4000]]
+    make = lambda i: Loop(lens[i], 3 + i, **shapes[i])
+    want = []
+    for i in range(4):
+        loop = make(i)
+        loop.calls()
+        want.append(loop.state())
+    for _ in range(3):
+        loops = [make(i) for i in range(4)]
+        streams = [torch.cuda.Stream() for _ in loops]
+        torch.cuda.synchronize()
+        with ThreadPoolExecutor(4) as pool:
+            list(pool.map(lambda x: x[0].calls(x[1]), zip(loops, streams)))
+        for i, loop in enumerate(loops):
+            assert same(loop.state(), want[i]), f"thread {i}"
