@@ -130,9 +130,12 @@ int mla_evict_select(const float* mass, int64_t mass_stride, const int32_t* seq_
   if (!aligned16(mass) || !aligned16(seq_lens) || !aligned16(budgets) || !aligned16(keep_idx) ||
       !aligned16(new_lens) || (dev_status && !aligned16(dev_status)))
     return MLA_ERR_MISALIGNED;
-  const Buffer lens = dense(new_lens, batch, 1, 4), keep = dense(keep_idx, batch, keep_stride, 4);
-  const Buffer read[] = {dense(mass, batch, mass_stride, 4), dense(seq_lens, batch, 1, 4), dense(budgets, batch, 1, 4)};
-  if (overlaps(lens, {keep}) || overlaps(lens, read) || overlaps(keep, read)) return MLA_ERR_INVALID_ARG;
+  // how much of a row of mass or keep_idx counts only the lengths say: the first element of each
+  const Buffer lens = dense(new_lens, batch, 1, 4), keep = strided(keep_idx, batch, 1, keep_stride, 4);
+  const Buffer sizes[] = {dense(seq_lens, batch, 1, 4), dense(budgets, batch, 1, 4)};
+  if (overlaps(lens, sizes) || overlaps(keep, sizes) || overlaps(keep, {lens}) ||
+      overlaps(strided(mass, batch, 1, mass_stride, 4), {lens, dense(keep_idx, 1, 1, 4)}))
+    return MLA_ERR_INVALID_ARG;
   int sms = 0, st = device_sms(&sms);
   if (st != MLA_OK) return st;
   mla::SelectArgs a;
@@ -159,7 +162,7 @@ int mla_cache_compact(const mla_dims* dims, mla_bf16* pool, const int32_t* page_
   const Buffer rows = dense(pool, (int64_t)num_pages * dims->page_size, dims->d_c + dims->d_rope, 2);
   const Buffer moved = strided(mass, batch, (int64_t)max_pages * dims->page_size, mass_stride, 4);
   const Buffer read[] = {dense(page_table, batch, max_pages, 4), dense(seq_lens, batch, 1, 4),
-                         dense(keep_idx, batch, keep_stride, 4), dense(new_lens, batch, 1, 4)};
+                         dense(new_lens, batch, 1, 4), dense(keep_idx, 1, 1, 4)};
   if (overlaps(moved, {rows}) || overlaps(moved, read) || overlaps(rows, read)) return MLA_ERR_INVALID_ARG;
   int sms = 0;
   if ((st = device_sms(&sms)) != MLA_OK) return st;

@@ -397,8 +397,10 @@ int mla_attn_mass(const mla_dims* dims, const mla_bf16* q_lat, const mla_bf16* p
  *              b * keep_stride, keep_stride >= min(L, budgets[b])
  *   new_lens   device int32 [batch] (output)
  *   dev_status device int32 word or NULL
- * keep_idx and new_lens must overlap neither each other nor an input
- * (MLA_ERR_INVALID_ARG): the lengths are read more than once while they are written.
+ * keep_idx and new_lens must overlap neither each other nor an input: lengths and masses
+ * are read more than once while they are written.  The call refuses (MLA_ERR_INVALID_ARG)
+ * what can be seen without the lengths: new_lens on seq_lens, on budgets or on the
+ * start of a row, and the start of a keep_idx row on any of the others.
  * A sequence whose length, budget or K is out of range records MLA_ERR_RANGE and
  * gets new_lens = 0.  batch <= 1024 and mass_stride <= 2^30 (else
  * MLA_ERR_UNSUPPORTED).
@@ -431,7 +433,8 @@ int mla_evict_select(const float* mass, int64_t mass_stride, const int32_t* seq_
  *   mass       device fp32 [batch, mass_stride] (updated in place) or NULL;
  *              mass_stride >= max_pages * page_size
  *   dev_status device int32 word or NULL
- * pool and mass must overlap neither each other nor an input (MLA_ERR_INVALID_ARG).
+ * pool and mass must overlap neither each other nor an input (MLA_ERR_INVALID_ARG; of
+ * keep_idx, whose lengths the host does not know, its first element counts).
  * Rows with keep_idx[b][j] == j are not touched.  An index outside [j, seq_lens[b])
  * records MLA_ERR_RANGE and leaves row j and its mass as they were.  A page outside the
  * pool, of n or of j, records it and leaves row j as it was; the mass, which lies in no

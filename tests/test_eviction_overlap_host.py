@@ -46,10 +46,11 @@ def cache_compact(lib, p, stride=TOKENS):
                                  p["new_lens"], B, PAGES, POOL, 1, p["mass"], stride, None, None)
 
 
-CALLS = {attn_mass: (["mass"], ["q_lat", "pool", "page_table", "seq_lens", "mass_lens", "lse"]),
-         evict_select: (["keep_idx", "new_lens"], ["mass", "seq_lens", "budgets"]),
-         cache_compact: (["pool", "mass"], ["page_table", "seq_lens", "keep_idx", "new_lens"])}
-PAIRS = [(call, out, other) for call, (outs, ins) in CALLS.items()
+# buffers whose used part the host knows: an output may not share a byte with another one
+KNOWN = {attn_mass: (["mass"], ["q_lat", "pool", "page_table", "seq_lens", "mass_lens", "lse"]),
+         evict_select: (["new_lens"], ["seq_lens", "budgets"]),
+         cache_compact: (["pool", "mass"], ["page_table", "seq_lens", "new_lens"])}
+PAIRS = [(call, out, other) for call, (outs, ins) in KNOWN.items()
          for out in outs for other in ins + outs if other != out]
 
 
@@ -63,6 +64,30 @@ def test_overlapping_output_is_refused(lib, call, out, other):
     # right before and right behind it lie other buffers: these calls get as far as the device
     for at in (p[other] + (BYTES[other] + 15) // 16 * 16, p[other] - (BYTES[out] + 15) // 16 * 16):
         assert call(lib, {**p, out: at}) == M.MLA_ERR_CUDA
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="fake addresses: only where nothing can be launched")
+@pytest.mark.parametrize("call,name,other", [
+    (evict_select, "keep_idx", "mass"), (evict_select, "keep_idx", "seq_lens"), (evict_select, "keep_idx", "budgets"),
+    (evict_select, "keep_idx", "new_lens"), (evict_select, "new_lens", "mass"), (evict_select, "new_lens", "keep_idx"),
+    (cache_compact, "pool", "keep_idx"), (cache_compact, "mass", "keep_idx"),
+], ids=lambda v: getattr(v, "__name__", v))
+def test_rows_of_a_length_unknown_to_the_host(lib, call, name, other):
+    # the same start is refused
+    p = addresses()
+    assert call(lib, {**p, name: p[other]}) == M.MLA_ERR_INVALID_ARG
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="fake addresses: only where nothing can be launched")
+def test_rows_of_mass_and_indices_may_take_turns(lib):
+    # one buffer of a row of mass and a row of indices for each sequence
+    p = addresses()
+    row = TOKENS + KEEP
+    p["keep_idx"] = p["mass"] + TOKENS * 4
+    assert lib.mla_evict_select(p["mass"], row, p["seq_lens"], p["budgets"], B, 0, 0, p["keep_idx"], row, p["new_lens"],
+                                None, None) == M.MLA_ERR_CUDA
+    assert lib.mla_cache_compact(ctypes.byref(DIMS), p["pool"], p["page_table"], p["seq_lens"], p["keep_idx"], row,
+                                 p["new_lens"], B, PAGES, POOL, 1, p["mass"], row, None, None) == M.MLA_ERR_CUDA
 
 
 @pytest.mark.skipif(torch.cuda.is_available(), reason="fake addresses: only where nothing can be launched")
