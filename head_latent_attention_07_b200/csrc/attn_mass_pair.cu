@@ -85,7 +85,8 @@ struct Bars {
   uint64_t drain;        // both: every MMA issued has completed
   uint32_t tmem_base;
   int abort;
-  int keyless;           // beside the lse: some row of the group saw no key (lse = -inf)
+  // beside the lse: the group's rows that saw a key (lse > -inf), 32 a word, and the full words
+  uint32_t has_key[8], full_words;
 };
 static_assert(Layout<256, false>::kOffBar + sizeof(Bars) <= Layout<256, false>::kOffRes, "barrier area");
 
@@ -166,7 +167,12 @@ struct Cursor {
     if (done) {
       if (left == 0) return false;
       int n;
-      while (tile >= (n = seq_tiles(p.m, b, &len))) { ++b; tile = 0; }
+      while (tile >= (n = seq_tiles(p.m, b, &len))) {
+        // (met only when another stream changes the lengths meanwhile: the roles' waits on one
+        // another then run out)
+        if (++b == p.m.batch) return false;
+        tile = 0;
+      }
       sub0 = t = tile;
       sub1 = kKeys ? tile + 1 : min(n, tile + left);
       if (!kKeys && p.groups > 1) sub1 = min(sub1, tile + kSubTiles);
@@ -374,17 +380,20 @@ attn_mass_pair_kernel(const __grid_constant__ CUtensorMap tq, const __grid_const
       const int cols = prm.rows_total - it.group * NT;
       const float* src = a.lse + (size_t)it.b * prm.rows_total + it.group * NT;
       float l[NT / 32];
-      bool keyless = false;
 #pragma unroll
-      for (int i = 0; i < NT / 32; ++i) {
-        l[i] = (i * 32 + lane < cols ? src[i * 32 + lane] : 0.f) * 1.4426950408889634f;
-        keyless |= l[i] == -INFINITY;
-      }
-      keyless = __any_sync(0xffffffffu, keyless);
+      for (int i = 0; i < NT / 32; ++i)
+        l[i] = i * 32 + lane < cols ? src[i * 32 + lane] * 1.4426950408889634f : -INFINITY;
       if (gi > 0 && !wwait(&bar->lse_empty, (gi - 1) & 1)) break;
 #pragma unroll
       for (int i = 0; i < NT / 32; ++i) lse2[i * 32 + lane] = l[i];
-      if (lane == 0) bar->keyless = keyless;
+      uint32_t full_words = 0;
+#pragma unroll
+      for (int i = 0; i < NT / 32; ++i) {
+        const uint32_t has_key = __ballot_sync(0xffffffffu, l[i] != -INFINITY);
+        if (lane == 0) bar->has_key[i] = has_key;
+        full_words |= has_key == ~0u ? 1u << i : 0u;
+      }
+      if (lane == 0) bar->full_words = full_words;
       __syncwarp();
       if (lane == 0) mbar_arrive(&bar->lse_full);
       ++gi;
@@ -410,7 +419,7 @@ attn_mass_pair_kernel(const __grid_constant__ CUtensorMap tq, const __grid_const
       return true;
     };
     int t = 0, gi = -1;
-    bool keyless = false;
+    uint32_t full_words = 0;
     float sum_so_far = 0.f;                      // what the key has collected
     bool more = fetch();
     while (more) {
@@ -428,23 +437,23 @@ attn_mass_pair_kernel(const __grid_constant__ CUtensorMap tq, const __grid_const
       if (kKeys || it.first) {
         ++gi;
         if (!wwait(&bar->lse_full, gi & 1)) break;
-        keyless = *static_cast<volatile int*>(&bar->keyless) != 0;
+        full_words = bar->full_words;
       }
       if (!wwait(&bar->acc_full[t & 1], (t >> 1) & 1)) break;
       tc_fence_after();
       const uint32_t acc = lanes + (t & 1) * NT;
       // key n is seen by query i when n <= len - nq + i: by query rows from H * (n - (len - nq)) on
       const int first = max(0, n - (it.len - a.nq)) * a.n_heads - it.group * NT;
-      // A row that saw no key gives nothing, whatever its query holds (padding: NaN too), so it is
-      // left out and not multiplied away; groups with such a row take the branch that looks.
-      const bool all = __all_sync(0xffffffffu, first <= 0) && !keyless;
+      const bool all = __all_sync(0xffffffffu, first <= 0);
       float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 1
       for (int c0 = 0; c0 < cols; c0 += 32) {
         float v[32];
         tmem_ld32(acc + c0, v);
         tmem_wait_ld();
-        if (all && c0 + 32 <= cols) {
+        // A row that saw no key gives nothing, whatever its query holds (padding: NaN too), so it is
+        // left out and not multiplied away.
+        if (all && (full_words >> (c0 / 32) & 1)) {
 #pragma unroll
           for (int i = 0; i < 32; i += 4) {
             const float4 l = *reinterpret_cast<const float4*>(lse2 + c0 + i);
@@ -454,10 +463,12 @@ attn_mass_pair_kernel(const __grid_constant__ CUtensorMap tq, const __grid_const
             sum[3] += ex2(fmaf(v[i + 3], prm.scale_log2, -l.w));
           }
         } else {
+          const uint32_t rows = bar->has_key[c0 / 32];
+          const uint32_t seen = first <= c0 ? rows : first >= c0 + 32 ? 0 : rows & (~0u << (first - c0));
 #pragma unroll
           for (int i = 0; i < 32; ++i) {
-            const float l = lse2[c0 + i], e = ex2(fmaf(v[i], prm.scale_log2, -l));
-            if (c0 + i >= first && c0 + i < cols && l != -INFINITY) sum[i & 3] += e;
+            const float e = ex2(fmaf(v[i], prm.scale_log2, -lse2[c0 + i]));
+            if (seen >> i & 1) sum[i & 3] += e;
           }
         }
       }
