@@ -529,8 +529,8 @@ cudaError_t launch(const CUtensorMap& tq, const CUtensorMap& tp, PairMassParams 
 
 }  // namespace
 
-// Wherever its loads can go: against the mma.sync kernel (pages of 48 tokens), 11.5 and 12.5 us
-// at 8 x 4096 with 32 heads, 103 and 454 at 16 x 32768 with 128.
+// Wherever its loads can go: against the mma.sync kernel (pages of 48 tokens), 13.2 and 13.8 us
+// at 8 x 4096 with 32 heads, 99 and 458 at 16 x 32768 with 128.
 bool attn_mass_pair_supported(const MassArgs& a) {
   return a.d_c + a.d_rope <= 64 * kMaxBlocks && a.page_size >= 8 && (a.page_size & (a.page_size - 1)) == 0 &&
          (int64_t)a.num_pages * a.page_size < INT32_MAX;   // a load's coordinates are 32 bits, its row past the pool too
