@@ -440,7 +440,7 @@ def mla_attn_mass(dims: MlaDims, q_lat, pool, page_table, seq_lens, lse, mass, m
                   dev_status=None, stream=None) -> None:
     """Add the attention weights of q_lat [B, nq, H, d_c+d_rope] (summed over query tokens
     and heads) to the cached tokens' mass [B, >= max_pages * page_size], the old mass times
-    `decay` first.  lse [B, nq, H] is mla_decode_attn's."""
+    `decay` first.  lse [B, nq, H] is mla_decode_attn's; rows with -inf give nothing."""
     torch = _torch()
     i32, f32, bf16 = torch.int32, torch.float32, torch.bfloat16
     B, nq = q_lat.shape[:2]
@@ -462,7 +462,8 @@ def mla_attn_mass(dims: MlaDims, q_lat, pool, page_table, seq_lens, lse, mass, m
 def mla_evict_select(mass, seq_lens, budgets, keep_idx, new_lens, n_sink: int = 0, n_recent: int = 0,
                      dev_status=None, stream=None) -> None:
     """keep_idx[b, :new_lens[b]] = the tokens of sequence b that stay within budgets[b]: the
-    first n_sink, the last n_recent and the largest of the rest by mass, ascending."""
+    first n_sink, the last n_recent and the largest of the rest by mass, ascending.
+    new_lens is a buffer of its own: seq_lens or budgets in its place are refused."""
     torch = _torch()
     i32 = torch.int32
     B = seq_lens.shape[0]
