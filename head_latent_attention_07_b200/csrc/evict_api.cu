@@ -65,6 +65,7 @@ bool overlaps(const Buffer& out, const Buffer (&others)[N]) {
   for (const Buffer& o : others) {
     if (o.p == nullptr) continue;
     const __int128 q = reinterpret_cast<uintptr_t>(o.p);
+    if (q >= p + (out.rows - 1) * out.stride + out.width || p >= q + o.width) continue;   // as a rule
     const __int128 row = q < p + out.width ? 0 : (q - p - out.width) / out.stride + 1;   // the first that ends behind q
     if (row < out.rows && p + row * out.stride < q + o.width) return true;
   }
